@@ -47,7 +47,9 @@ EXPORTED = (
     "fno_mse", "fno_profile_enable", "fno_profile_read", "fno_set_tensor_cores",
     "fno_device_error", "fno_spectral_conv_fwd_noalloc", "fno_adam_step",
     "fno_backward_ready", "fno_spectral_conv_fwd_cp", "fno_block_fwd_cp", "fno_set_wait_limit",
-    "fno_spectral_conv_bwd_cp", "fno_block_bwd_cp",
+    "fno_spectral_conv_bwd_cp", "fno_block_bwd_cp", "fno_layer_norm_workspace_size",
+    "fno_layer_norm_fwd", "fno_layer_norm_bwd", "fno_grad_norm_workspace_size", "fno_grad_norm",
+    "fno_clip_grads", "fno_adam_step_clipped",
 )
 
 FNO_MAX_CP_RANK = 32
@@ -82,6 +84,11 @@ class NetDesc(ctypes.Structure):
     ]
 
 
+class NormDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("channels", ctypes.c_int), ("outer", ctypes.c_int64),
+                ("inner", ctypes.c_int64), ("eps", ctypes.c_float)]
+
+
 _PARR = ctypes.c_void_p * FNO_MAX_LAYERS
 
 
@@ -110,6 +117,7 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib = ctypes.CDLL(path)
     vp, sz, i = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
     bd, nd = ctypes.POINTER(BlockDesc), ctypes.POINTER(NetDesc)
+    ld, f = ctypes.POINTER(NormDesc), ctypes.c_float
     sig = {
         "fno_last_error": (ctypes.c_char_p, []),
         "fno_version": (ctypes.c_char_p, []),
@@ -141,6 +149,14 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         "fno_adam_step": (i, [ctypes.c_int64, vp, vp, vp, vp, vp, i, i, ctypes.c_float,
                               ctypes.c_float, ctypes.c_float, ctypes.c_float, ctypes.c_float,
                               ctypes.c_float, vp]),
+        "fno_adam_step_clipped": (i, [ctypes.c_int64, vp, vp, vp, vp, vp, i, i, f, f, f, f, f, f,
+                                      vp, i, vp]),
+        "fno_layer_norm_workspace_size": (sz, [ld]),
+        "fno_layer_norm_fwd": (i, [ld, vp, vp, vp, vp, vp, vp, vp]),
+        "fno_layer_norm_bwd": (i, [ld, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "fno_grad_norm_workspace_size": (sz, [i]),
+        "fno_grad_norm": (i, [i, vp, vp, i, f, f, vp, vp, sz, vp]),
+        "fno_clip_grads": (i, [i, vp, vp, vp, i, f, f, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -450,3 +466,247 @@ def fno_adam_step(theta, m, v, grad, param_out, step: int, lr: float, beta1: flo
                                 _ptr(param_out), out_code, int(step), float(lr), float(beta1),
                                 float(beta2), float(eps), float(weight_decay), float(grad_scale),
                                 _stream(stream)))
+
+
+def fno_adam_step_clipped(theta, m, v, grad, param_out, step: int, lr: float, norm,
+                          beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+                          weight_decay: float = 0.0, grad_scale: float = 1.0,
+                          skip_nonfinite: bool = False, stream=None):
+    """:func:`fno_adam_step` with the gradient also multiplied by ``norm[1]``
+    (float32 device tensor of two, from :func:`fno_grad_norm`).
+    ``skip_nonfinite``: a norm that is not finite leaves the state as it is."""
+    out_code = _dtype_code_of(param_out) if param_out is not None else FNO_F32
+    n, dev = theta.numel(), theta.device
+    for t, name in ((theta, "theta"), (m, "m"), (v, "v"), (grad, "grad")):
+        _check_tensor(t, name, FNO_F32, n, dev)
+    if param_out is not None:
+        _check_tensor(param_out, "param_out", out_code, n, dev)
+    _check_tensor(norm, "norm", FNO_F32, 2, dev)
+    with _On(dev, stream) as st:
+        _check(load().fno_adam_step_clipped(n, _ptr(theta), _ptr(m), _ptr(v), _ptr(grad),
+                                            _ptr(param_out), out_code, int(step), float(lr),
+                                            float(beta1), float(beta2), float(eps),
+                                            float(weight_decay), float(grad_scale), _ptr(norm),
+                                            1 if skip_nonfinite else 0, st))
+
+
+# --------------------------------------------------------------------------
+# layer normalisation, gradient norm and clipping
+# --------------------------------------------------------------------------
+
+def _torch_dtypes():
+    """torch dtype of each storage code (filled on first use: importing this
+    module does not import torch)."""
+    global _TORCH_DTYPES
+    if _TORCH_DTYPES is None:
+        import torch
+        _TORCH_DTYPES = (torch.float32, torch.float16, torch.bfloat16)
+    return _TORCH_DTYPES
+
+
+_TORCH_DTYPES = None
+
+
+def _check_tensor(t, name: str, code: int, numel: int, device=None) -> None:
+    if t.dtype != _torch_dtypes()[code]:
+        raise ValueError(f"{name} is {t.dtype}, expected {_torch_dtypes()[code]}")
+    if t.numel() != numel:
+        raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _scratch(nbytes: int, device, ws, stream):
+    """The caller's workspace, or a fresh one that is not reused before the work
+    of the given stream is done with it."""
+    import torch
+    if ws is not None:
+        if ws.device != device:
+            raise ValueError(f"ws is on {ws.device}, expected {device}")
+        return ws, ws.numel() * ws.element_size()
+    ws, nb = _workspace(nbytes, device, None)
+    if stream is not None and ws.is_cuda:
+        ws.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                         else torch.cuda.ExternalStream(stream, device=device))
+    return ws, nb
+
+
+class _On:
+    """The tensors' device as the current one for a call, and the stream to use:
+    the given one, else that device's current stream."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.guard = None
+        if device.type == "cuda" and device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(device)
+        self.stream = stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def layer_norm_desc(outer: int, channels: int, inner: int = 1, dtype: str = "f32",
+                    eps: float = 1e-5) -> NormDesc:
+    """Layer norm over ``channels`` of x [outer][channels][inner] (activations:
+    outer = batch, inner = grid points; inner = 1: rows)."""
+    d = NormDesc()
+    d.dtype = DTYPE_CODE[dtype]
+    d.channels, d.outer, d.inner, d.eps = int(channels), int(outer), int(inner), float(eps)
+    return d
+
+
+def fno_layer_norm_workspace_size(desc: NormDesc) -> int:
+    n = load().fno_layer_norm_workspace_size(ctypes.byref(desc))
+    if n == 0:
+        raise FnoError(FNO_ERR_INVALID_ARG, last_error())
+    return n
+
+
+def _check_norm_tensors(desc: NormDesc, big, channel, stats, grads=()):
+    dev = big[0][0].device
+    points = desc.outer * desc.inner
+    for t, name in big:
+        _check_tensor(t, name, desc.dtype, points * desc.channels, dev)
+    for t, name in channel:
+        if t is not None:
+            _check_tensor(t, name, desc.dtype, desc.channels, dev)
+    for t, name in stats:
+        if t is not None:
+            _check_tensor(t, name, FNO_F32, points, dev)
+    for t, name in grads:
+        if t is not None:
+            _check_tensor(t, name, FNO_F32, desc.channels, dev)
+    return dev
+
+
+def fno_layer_norm_fwd(desc: NormDesc, x, gamma, beta, y, mean=None, rstd=None, stream=None):
+    """y = (x - mean) rstd gamma + beta over the channels; ``y`` may be ``x``.
+    ``gamma`` / ``beta`` None: 1 / 0.  ``mean``, ``rstd`` (float32, [outer][inner]):
+    what the backward reads."""
+    dev = _check_norm_tensors(desc, ((x, "x"), (y, "y")), ((gamma, "gamma"), (beta, "beta")),
+                              ((mean, "mean"), (rstd, "rstd")))
+    with _On(dev, stream) as st:
+        _check(load().fno_layer_norm_fwd(ctypes.byref(desc), _ptr(x), _ptr(gamma), _ptr(beta),
+                                         _ptr(y), _ptr(mean), _ptr(rstd), st))
+    return y
+
+
+def fno_layer_norm_bwd(desc: NormDesc, x, gamma, mean, rstd, dy, dx, dgamma=None, dbeta=None,
+                       ws=None, stream=None):
+    """Adjoint of :func:`fno_layer_norm_fwd`: dx (may be ``dy``) and, where given,
+    dgamma and dbeta (float32)."""
+    dev = _check_norm_tensors(desc, ((x, "x"), (dy, "dy"), (dx, "dx")), ((gamma, "gamma"),),
+                              ((mean, "mean"), (rstd, "rstd")),
+                              ((dgamma, "dgamma"), (dbeta, "dbeta")))
+    with _On(dev, stream) as st:
+        nb = 0
+        if dgamma is not None or dbeta is not None:
+            ws, nb = _scratch(fno_layer_norm_workspace_size(desc) if ws is None else 0, dev, ws,
+                              stream)
+        _check(load().fno_layer_norm_bwd(ctypes.byref(desc), _ptr(x), _ptr(gamma), _ptr(mean),
+                                         _ptr(rstd), _ptr(dy), _ptr(dx), _ptr(dgamma),
+                                         _ptr(dbeta), _ptr(ws), nb, st))
+    return dx, dgamma, dbeta
+
+
+class GradList:
+    """Gradients of one dtype and device, and where their clipped values go: the
+    pointer and size arrays of the C calls, built once by :func:`grad_list`.
+    The tensors must stay in place while the list is used."""
+
+    def __init__(self, grads, out=None):
+        grads = list(grads)
+        if not grads:
+            raise ValueError("no gradients given")
+        self.dtype = _dtype_code_of(grads[0])
+        self.device = grads[0].device
+        targets = grads if out is None else list(out)
+        if len(targets) != len(grads):
+            raise ValueError(f"{len(targets)} outputs for {len(grads)} gradients")
+        for k, (g, o) in enumerate(zip(grads, targets)):
+            _check_tensor(g, f"grads[{k}]", self.dtype, g.numel(), self.device)
+            _check_tensor(o, f"out[{k}]", self.dtype, g.numel(), self.device)
+        n = len(grads)
+        self.n = n
+        self.tensors = (grads, targets)     # keeps the memory alive
+        self.sizes = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
+        self.grads = (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads])
+        self.out = (ctypes.c_void_p * n)(*[o.data_ptr() for o in targets])
+        self._check_overlaps()
+
+    def _check_overlaps(self) -> None:
+        """Every target must be its own gradient or disjoint from all the rest."""
+        grads, targets = self.tensors
+        size = grads[0].element_size()
+        spans = []
+        for k, (g, o) in enumerate(zip(grads, targets)):
+            if g.numel() == 0:
+                continue
+            nb = g.numel() * size
+            spans.append((o.data_ptr(), o.data_ptr() + nb, True, k))
+            if g.data_ptr() != o.data_ptr():
+                spans.append((g.data_ptr(), g.data_ptr() + nb, False, k))
+        spans.sort()
+        end, end_written = 0, 0      # furthest ends so far: of all, and of the written ones
+        for lo, hi, written, k in spans:
+            if lo < (end if written else end_written):
+                raise ValueError(f"the memory of tensor {k} overlaps another one's")
+            end = max(end, hi)
+            if written:
+                end_written = max(end_written, hi)
+
+
+def grad_list(grads, out=None) -> GradList:
+    """The list of gradients for :func:`fno_grad_norm` and :func:`fno_clip_grads`;
+    ``out``: tensors for the clipped gradients (default: in place)."""
+    return GradList(grads, out)
+
+
+def _as_grad_list(grads) -> GradList:
+    return grads if isinstance(grads, GradList) else GradList(grads)
+
+
+def fno_grad_norm_workspace_size(grads) -> int:
+    """Workspace bytes for a :class:`GradList`, a sequence of tensors, or a count."""
+    n = grads.n if isinstance(grads, GradList) else grads if isinstance(grads, int) else len(grads)
+    nb = load().fno_grad_norm_workspace_size(n)
+    if nb == 0:
+        raise FnoError(FNO_ERR_INVALID_ARG, last_error())
+    return nb
+
+
+def fno_grad_norm(grads, max_norm: float, norm, grad_scale: float = 1.0, ws=None, stream=None):
+    """``norm`` (float32 device tensor of two) receives the global norm of
+    ``grad_scale`` times the gradients and the factor min(1, max_norm / norm).
+    ``grads``: a :class:`GradList` or a sequence of tensors."""
+    gl = _as_grad_list(grads)
+    _check_tensor(norm, "norm", FNO_F32, 2, gl.device)
+    with _On(gl.device, stream) as st:
+        ws, nb = _scratch(fno_grad_norm_workspace_size(gl) if ws is None else 0, gl.device, ws,
+                          stream)
+        _check(load().fno_grad_norm(gl.n, gl.grads, gl.sizes, gl.dtype, float(grad_scale),
+                                    float(max_norm), _ptr(norm), _ptr(ws), nb, st))
+    return norm
+
+
+def fno_clip_grads(grads, max_norm: float, norm, grad_scale: float = 1.0, ws=None, stream=None):
+    """:func:`fno_grad_norm`, then every gradient times ``grad_scale * norm[1]``,
+    in place or into the list's ``out`` tensors."""
+    gl = _as_grad_list(grads)
+    _check_tensor(norm, "norm", FNO_F32, 2, gl.device)
+    with _On(gl.device, stream) as st:
+        ws, nb = _scratch(fno_grad_norm_workspace_size(gl) if ws is None else 0, gl.device, ws,
+                          stream)
+        _check(load().fno_clip_grads(gl.n, gl.grads, gl.out, gl.sizes, gl.dtype,
+                                     float(grad_scale), float(max_norm), _ptr(norm), _ptr(ws), nb,
+                                     st))
+    return norm

@@ -40,6 +40,7 @@ int cuda_fail(cudaError_t e, const char *where) {
   } while (0)
 
 constexpr size_t kSmemLimit = 227 * 1024;
+constexpr int64_t kMaxElements = 1LL << 40;   // of one layer norm or list of gradients
 
 size_t elsize(int dtype) { return dtype == FNO_F32 ? 4 : 2; }
 size_t al(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -994,9 +995,10 @@ int fno_mse(int64_t n, int dtype, const void *u, const void *target, float *loss
   return FNO_OK;
 }
 
-int fno_adam_step(int64_t n, float *theta, float *m, float *v, const float *grad,
-                  void *param_out, int out_dtype, int step, float lr, float beta1, float beta2,
-                  float eps, float weight_decay, float grad_scale, fno_stream_t stream) {
+static int adam_step(int64_t n, float *theta, float *m, float *v, const float *grad,
+                     void *param_out, int out_dtype, int step, float lr, float beta1,
+                     float beta2, float eps, float weight_decay, float grad_scale,
+                     const float *norm, bool skip_nonfinite, fno_stream_t stream) {
   if (n < 1) return fail(FNO_ERR_INVALID_ARG, "n %lld < 1", (long long)n);
   REQUIRE_PTR(theta, "theta");
   OPTIONAL_PTR(param_out, "param_out");
@@ -1030,8 +1032,189 @@ int fno_adam_step(int64_t n, float *theta, float *m, float *v, const float *grad
   }
   Launch L = make_launch(stream);
   FNO_TRY(launch_adam(L, n, theta, grad ? m : nullptr, grad ? v : nullptr, grad, param_out,
-                      out_dtype, c),
+                      out_dtype, c, norm, skip_nonfinite),
           "adam");
+  g_err[0] = 0;
+  return FNO_OK;
+}
+
+int fno_adam_step(int64_t n, float *theta, float *m, float *v, const float *grad,
+                  void *param_out, int out_dtype, int step, float lr, float beta1, float beta2,
+                  float eps, float weight_decay, float grad_scale, fno_stream_t stream) {
+  return adam_step(n, theta, m, v, grad, param_out, out_dtype, step, lr, beta1, beta2, eps,
+                   weight_decay, grad_scale, nullptr, false, stream);
+}
+
+int fno_adam_step_clipped(int64_t n, float *theta, float *m, float *v, const float *grad,
+                          void *param_out, int out_dtype, int step, float lr, float beta1,
+                          float beta2, float eps, float weight_decay, float grad_scale,
+                          const float *norm, int skip_nonfinite, fno_stream_t stream) {
+  REQUIRE_PTR(grad, "grad");
+  if (!norm) return fail(FNO_ERR_INVALID_ARG, "norm is NULL");
+  if ((uintptr_t)norm & 3) return fail(FNO_ERR_INVALID_ARG, "norm is not 4-byte aligned");
+  return adam_step(n, theta, m, v, grad, param_out, out_dtype, step, lr, beta1, beta2, eps,
+                   weight_decay, grad_scale, norm, skip_nonfinite != 0, stream);
+}
+
+// ---------------------------------------------------------------------------
+// layer normalisation
+// ---------------------------------------------------------------------------
+
+static int check_norm(const fno_norm_desc *d, NormShape *s) {
+  if (!d) return fail(FNO_ERR_INVALID_ARG, "descriptor is NULL");
+  if (d->dtype < FNO_F32 || d->dtype > FNO_BF16)
+    return fail(FNO_ERR_INVALID_ARG, "dtype %d unknown", d->dtype);
+  if (d->outer < 1 || d->inner < 1 || d->channels < 1)
+    return fail(FNO_ERR_INVALID_ARG, "outer %lld, channels %d, inner %lld must be >= 1",
+                (long long)d->outer, d->channels, (long long)d->inner);
+  if (d->channels > FNO_MAX_NORM_CHANNELS)
+    return fail(FNO_ERR_UNSUPPORTED, "channels %d exceed %d", d->channels, FNO_MAX_NORM_CHANNELS);
+  if (d->outer > kMaxElements || d->inner > kMaxElements / d->outer ||
+      d->channels > kMaxElements / d->outer / d->inner)
+    return fail(FNO_ERR_UNSUPPORTED, "more than 2^40 elements");
+  if (!(d->eps > 0.f) || !isfinite(d->eps))
+    return fail(FNO_ERR_INVALID_ARG, "eps %g <= 0", d->eps);
+  *s = NormShape{d->outer, d->inner, d->channels, d->eps};
+  return FNO_OK;
+}
+
+size_t fno_layer_norm_workspace_size(const fno_norm_desc *desc) {
+  NormShape s;
+  if (check_norm(desc, &s)) return 0;
+  g_err[0] = 0;
+  return al(ln_partial_bytes(s.C));
+}
+
+int fno_layer_norm_fwd(const fno_norm_desc *desc, const void *x, const void *gamma,
+                       const void *beta, void *y, float *mean, float *rstd,
+                       fno_stream_t stream) {
+  NormShape s;
+  int rc = check_norm(desc, &s);
+  if (rc) return rc;
+  REQUIRE_PTR(x, "x");
+  OPTIONAL_PTR(gamma, "gamma");
+  OPTIONAL_PTR(beta, "beta");
+  REQUIRE_PTR(y, "y");
+  OPTIONAL_PTR(mean, "mean");
+  OPTIONAL_PTR(rstd, "rstd");
+  if (!mean != !rstd)
+    return fail(FNO_ERR_INVALID_ARG, "mean and rstd: give both or neither");
+  Launch L = make_launch(stream);
+  FNO_TRY(launch_ln_fwd(L, s, desc->dtype, x, gamma, beta, y, mean, rstd), "layer norm");
+  g_err[0] = 0;
+  return FNO_OK;
+}
+
+int fno_layer_norm_bwd(const fno_norm_desc *desc, const void *x, const void *gamma,
+                       const float *mean, const float *rstd, const void *dy, void *dx,
+                       float *dgamma, float *dbeta, void *ws, size_t ws_bytes,
+                       fno_stream_t stream) {
+  NormShape s;
+  int rc = check_norm(desc, &s);
+  if (rc) return rc;
+  REQUIRE_PTR(x, "x");
+  OPTIONAL_PTR(gamma, "gamma");
+  REQUIRE_PTR(mean, "mean");
+  REQUIRE_PTR(rstd, "rstd");
+  REQUIRE_PTR(dy, "dy");
+  REQUIRE_PTR(dx, "dx");
+  if (dx == x) return fail(FNO_ERR_INVALID_ARG, "dx overlaps x");
+  OPTIONAL_PTR(dgamma, "dgamma");
+  OPTIONAL_PTR(dbeta, "dbeta");
+  if (dgamma || dbeta) {
+    const size_t need = al(ln_partial_bytes(s.C));
+    if (ws_bytes < need)
+      return fail(FNO_ERR_WORKSPACE, "workspace %zu B < %zu B", ws_bytes, need);
+    REQUIRE_PTR(ws, "ws");
+  }
+  Launch L = make_launch(stream);
+  FNO_TRY(launch_ln_bwd(L, s, desc->dtype, x, gamma, mean, rstd, dy, dx, dgamma, dbeta,
+                        reinterpret_cast<float *>(ws)),
+          "layer norm backward");
+  g_err[0] = 0;
+  return FNO_OK;
+}
+
+// ---------------------------------------------------------------------------
+// gradient norm and clipping
+// ---------------------------------------------------------------------------
+
+static size_t grad_norm_ws(int n_tensors) {
+  const size_t launches = ((size_t)n_tensors + kClipTensors - 1) / kClipTensors;
+  return al(sizeof(double) * kNormCTAs * launches);
+}
+
+size_t fno_grad_norm_workspace_size(int n_tensors) {
+  if (n_tensors < 1) {
+    fail(FNO_ERR_INVALID_ARG, "n_tensors %d < 1", n_tensors);
+    return 0;
+  }
+  g_err[0] = 0;
+  return grad_norm_ws(n_tensors);
+}
+
+static int check_grads(int n, const void *const *grads, void *const *out, const int64_t *sizes,
+                       int dtype, float grad_scale, float max_norm, const float *norm,
+                       const void *ws, size_t ws_bytes) {
+  if (n < 1) return fail(FNO_ERR_INVALID_ARG, "n_tensors %d < 1", n);
+  if (!grads) return fail(FNO_ERR_INVALID_ARG, "grads is NULL");
+  if (!sizes) return fail(FNO_ERR_INVALID_ARG, "sizes is NULL");
+  if (dtype < FNO_F32 || dtype > FNO_BF16)
+    return fail(FNO_ERR_INVALID_ARG, "dtype %d unknown", dtype);
+  const uintptr_t mask = elsize(dtype) - 1;
+  long long total = 0;
+  for (int i = 0; i < n; ++i) {
+    if (sizes[i] < 0)
+      return fail(FNO_ERR_INVALID_ARG, "sizes[%d] = %lld < 0", i, (long long)sizes[i]);
+    if (sizes[i] == 0) continue;
+    if (sizes[i] > kMaxElements - total)
+      return fail(FNO_ERR_UNSUPPORTED, "more than 2^40 elements");
+    total += sizes[i];
+    if (!grads[i]) return fail(FNO_ERR_INVALID_ARG, "grads[%d] is NULL", i);
+    if ((uintptr_t)grads[i] & mask)
+      return fail(FNO_ERR_INVALID_ARG, "grads[%d] is not aligned to its elements", i);
+    if (!out) continue;
+    if (!out[i]) return fail(FNO_ERR_INVALID_ARG, "out[%d] is NULL", i);
+    if ((uintptr_t)out[i] & mask)
+      return fail(FNO_ERR_INVALID_ARG, "out[%d] is not aligned to its elements", i);
+  }
+  if (!isfinite(grad_scale)) return fail(FNO_ERR_INVALID_ARG, "grad_scale is not finite");
+  if (!(max_norm >= 0.f)) return fail(FNO_ERR_INVALID_ARG, "max_norm %g < 0", max_norm);
+  if (!norm) return fail(FNO_ERR_INVALID_ARG, "norm is NULL");
+  if ((uintptr_t)norm & 3) return fail(FNO_ERR_INVALID_ARG, "norm is not 4-byte aligned");
+  const size_t need = grad_norm_ws(n);
+  if (ws_bytes < need) return fail(FNO_ERR_WORKSPACE, "workspace %zu B < %zu B", ws_bytes, need);
+  REQUIRE_PTR(ws, "ws");
+  return FNO_OK;
+}
+
+int fno_grad_norm(int n_tensors, const void *const *grads, const int64_t *sizes, int dtype,
+                  float grad_scale, float max_norm, float *norm, void *ws, size_t ws_bytes,
+                  fno_stream_t stream) {
+  int rc = check_grads(n_tensors, grads, nullptr, sizes, dtype, grad_scale, max_norm, norm, ws,
+                       ws_bytes);
+  if (rc) return rc;
+  Launch L = make_launch(stream);
+  FNO_TRY(launch_grad_norm(L, n_tensors, grads, sizes, dtype, grad_scale, max_norm, norm,
+                           reinterpret_cast<double *>(ws)),
+          "gradient norm");
+  g_err[0] = 0;
+  return FNO_OK;
+}
+
+int fno_clip_grads(int n_tensors, const void *const *grads, void *const *out,
+                   const int64_t *sizes, int dtype, float grad_scale, float max_norm, float *norm,
+                   void *ws, size_t ws_bytes, fno_stream_t stream) {
+  if (!out) return fail(FNO_ERR_INVALID_ARG, "out is NULL");
+  int rc = check_grads(n_tensors, grads, out, sizes, dtype, grad_scale, max_norm, norm, ws,
+                       ws_bytes);
+  if (rc) return rc;
+  Launch L = make_launch(stream);
+  FNO_TRY(launch_grad_norm(L, n_tensors, grads, sizes, dtype, grad_scale, max_norm, norm,
+                           reinterpret_cast<double *>(ws)),
+          "gradient norm");
+  FNO_TRY(launch_grad_scale(L, n_tensors, grads, out, sizes, dtype, grad_scale, norm),
+          "gradient clipping");
   g_err[0] = 0;
   return FNO_OK;
 }

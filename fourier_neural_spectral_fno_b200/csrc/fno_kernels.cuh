@@ -262,7 +262,41 @@ struct AdamCoef {
   float inv_bc1, inv_bc2;   // 1 / (1 - beta^t)
   float eps, lr_wd, grad_scale;
 };
+// clip (optional, device): (norm, factor) as launch_grad_norm writes them; the
+// gradient is multiplied by the factor, and with skip_nonfinite a norm that is
+// not finite leaves theta, m and v as they are (out is still written)
 cudaError_t launch_adam(const Launch &L, long long n, float *theta, float *m, float *v,
-                        const float *g, void *out, int out_dtype, const AdamCoef &c);
+                        const float *g, void *out, int out_dtype, const AdamCoef &c,
+                        const float *clip = nullptr, bool skip_nonfinite = false);
+
+// ---- layer normalisation (norm.cu) ----------------------------------------
+// over the C channels of x [outer][C][inner]
+struct NormShape {
+  long long outer, inner;
+  int C;
+  float eps;
+};
+size_t ln_partial_bytes(int C);
+// gamma, beta may be NULL (1, 0); mean, rstd [outer][inner] both or neither; y may be x
+cudaError_t launch_ln_fwd(const Launch &L, const NormShape &s, int dtype, const void *x,
+                          const void *gamma, const void *beta, void *y, float *mean,
+                          float *rstd);
+// dgamma, dbeta may be NULL; dx may be dy; partial: ln_partial_bytes(C)
+cudaError_t launch_ln_bwd(const Launch &L, const NormShape &s, int dtype, const void *x,
+                          const void *gamma, const float *mean, const float *rstd, const void *dy,
+                          void *dx, float *dgamma, float *dbeta, float *partial);
+
+// ---- gradient norm and clipping (clip.cu) ----------------------------------
+constexpr int kClipTensors = 128;   // tensors of one launch (a 4 KB parameter block)
+constexpr int kNormCTAs = 1184;     // most partial sums of one launch
+// norm (device): [0] = |grad_scale| ||g||, [1] = min(1, max_norm / norm);
+// partial: kNormCTAs float64 for each kClipTensors tensors
+cudaError_t launch_grad_norm(const Launch &L, int n, const void *const *grads,
+                             const int64_t *sizes, int dtype, float grad_scale, float max_norm,
+                             float *norm, double *partial);
+// out[i] = grads[i] grad_scale norm[1]
+cudaError_t launch_grad_scale(const Launch &L, int n, const void *const *grads, void *const *out,
+                              const int64_t *sizes, int dtype, float grad_scale,
+                              const float *norm);
 
 }  // namespace fno

@@ -1,0 +1,289 @@
+// Layer normalisation over the channel axis of x [outer][C][inner], forward and
+// backward.  A point is one (outer, inner) pair; its C values lie `inner`
+// elements apart.
+//   mean = sum_c x / C,  var = sum_c (x - mean)^2 / C,  rstd = 1 / sqrt(var + eps)
+//   xh = (x - mean) rstd,  y = xh gamma + beta
+//   g = dy gamma,  dx = rstd (g - mean_c(g) - xh mean_c(g xh))
+//   dgamma[c] = sum_points dy xh,  dbeta[c] = sum_points dy
+// All sums are float32.  The variance is taken about a first mean m0 in a second
+// sweep over the values, which also gives e = mean(x - m0), the rounding of m0:
+// mean = m0 + e, var = mean((x - m0)^2) - e^2, xh = ((x - m0) - e) rstd, so a
+// common offset far above the spread costs no more than the offset's own storage.
+#include "fno_common.cuh"
+#include "fno_kernels.cuh"
+
+namespace fno {
+
+namespace {
+
+constexpr int LT = 256;
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// sum over the CTA of LT threads, the same value in every thread
+__device__ __forceinline__ float cta_sum(float v, float *sh) {
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float t = 0.f;
+#pragma unroll
+  for (int i = 0; i < LT / 32; ++i) t += sh[i];
+  __syncthreads();
+  return t;
+}
+
+// ---------------------------------------------------------------------------
+// any channel count: the values are read again in each sweep
+// ---------------------------------------------------------------------------
+
+// thread per point (inner > 1: neighbouring threads read neighbouring points)
+template <typename T>
+__global__ void __launch_bounds__(LT)
+    k_ln_fwd_point(const T *x, const T *__restrict__ gamma, const T *__restrict__ beta, T *y,
+                   float *__restrict__ mean, float *__restrict__ rstd, long long points, int C,
+                   long long inner, float inv_c, float eps) {
+  const long long stride = (long long)gridDim.x * LT;
+  for (long long p = (long long)blockIdx.x * LT + threadIdx.x; p < points; p += stride) {
+    const long long b = p / inner, base = b * C * inner + (p - b * inner);
+    float m0 = 0.f;
+    for (int c = 0; c < C; ++c) m0 += to_f<T>(x[base + c * inner]);
+    m0 *= inv_c;
+    float e = 0.f, q = 0.f;
+    for (int c = 0; c < C; ++c) {
+      const float d = to_f<T>(x[base + c * inner]) - m0;
+      e += d;
+      q = fmaf(d, d, q);
+    }
+    e *= inv_c;
+    const float var = fmaxf(fmaf(-e, e, q * inv_c), 0.f);
+    const float r = 1.0f / sqrtf((q != q ? q : var) + eps);
+    if (mean) {
+      mean[p] = m0 + e;
+      rstd[p] = r;
+    }
+    for (int c = 0; c < C; ++c) {
+      const float xh = ((to_f<T>(x[base + c * inner]) - m0) - e) * r;
+      y[base + c * inner] = from_f<T>(fmaf(xh, gamma ? to_f<T>(gamma[c]) : 1.f,
+                                           beta ? to_f<T>(beta[c]) : 0.f));
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(LT)
+    k_ln_bwd_point(const T *__restrict__ x, const T *__restrict__ gamma,
+                   const float *__restrict__ mean, const float *__restrict__ rstd, const T *dy,
+                   T *dx, long long points, int C, long long inner, float inv_c) {
+  const long long stride = (long long)gridDim.x * LT;
+  for (long long p = (long long)blockIdx.x * LT + threadIdx.x; p < points; p += stride) {
+    const long long b = p / inner, base = b * C * inner + (p - b * inner);
+    const float mu = mean[p], r = rstd[p];
+    float c1 = 0.f, c2 = 0.f;
+    for (int c = 0; c < C; ++c) {
+      const float g = to_f<T>(dy[base + c * inner]) * (gamma ? to_f<T>(gamma[c]) : 1.f);
+      c1 += g;
+      c2 = fmaf(g, (to_f<T>(x[base + c * inner]) - mu) * r, c2);
+    }
+    c1 *= inv_c;
+    c2 *= inv_c;
+    for (int c = 0; c < C; ++c) {
+      const float g = to_f<T>(dy[base + c * inner]) * (gamma ? to_f<T>(gamma[c]) : 1.f);
+      const float xh = (to_f<T>(x[base + c * inner]) - mu) * r;
+      dx[base + c * inner] = from_f<T>(r * (g - c1 - xh * c2));
+    }
+  }
+}
+
+// CTA per (channel, slice of the points): partial[slice][c] = (dgamma, dbeta)
+template <typename T>
+__global__ void __launch_bounds__(LT)
+    k_ln_dparam_point(const T *__restrict__ x, const float *__restrict__ mean,
+                      const float *__restrict__ rstd, const T *__restrict__ dy,
+                      float *__restrict__ partial, long long points, int C, long long inner) {
+  __shared__ float sh[LT / 32];
+  const int c = blockIdx.x, slices = gridDim.y, sl = blockIdx.y;
+  float dg = 0.f, db = 0.f;
+  for (long long p = (long long)sl * LT + threadIdx.x; p < points; p += (long long)slices * LT) {
+    const long long b = p / inner, i = (b * C + c) * inner + (p - b * inner);
+    const float d = to_f<T>(dy[i]);
+    dg = fmaf(d, (to_f<T>(x[i]) - mean[p]) * rstd[p], dg);
+    db += d;
+  }
+  dg = cta_sum(dg, sh);
+  db = cta_sum(db, sh);
+  if (threadIdx.x == 0) {
+    partial[((long long)sl * C + c) * 2] = dg;
+    partial[((long long)sl * C + c) * 2 + 1] = db;
+  }
+}
+
+// CTA per row (inner == 1)
+template <typename T>
+__global__ void __launch_bounds__(LT)
+    k_ln_fwd_row(const T *x, const T *__restrict__ gamma, const T *__restrict__ beta, T *y,
+                 float *__restrict__ mean, float *__restrict__ rstd, long long rows, int C,
+                 float inv_c, float eps) {
+  __shared__ float sh[LT / 32];
+  for (long long p = blockIdx.x; p < rows; p += gridDim.x) {
+    const T *xr = x + p * C;
+    T *yr = y + p * C;
+    float m0 = 0.f;
+    for (int c = threadIdx.x; c < C; c += LT) m0 += to_f<T>(xr[c]);
+    m0 = cta_sum(m0, sh) * inv_c;
+    float e = 0.f, q = 0.f;
+    for (int c = threadIdx.x; c < C; c += LT) {
+      const float d = to_f<T>(xr[c]) - m0;
+      e += d;
+      q = fmaf(d, d, q);
+    }
+    e = cta_sum(e, sh) * inv_c;
+    q = cta_sum(q, sh);
+    const float var = fmaxf(fmaf(-e, e, q * inv_c), 0.f);
+    const float r = 1.0f / sqrtf((q != q ? q : var) + eps);
+    if (mean && threadIdx.x == 0) {
+      mean[p] = m0 + e;
+      rstd[p] = r;
+    }
+    for (int c = threadIdx.x; c < C; c += LT) {
+      const float xh = ((to_f<T>(xr[c]) - m0) - e) * r;
+      yr[c] = from_f<T>(fmaf(xh, gamma ? to_f<T>(gamma[c]) : 1.f, beta ? to_f<T>(beta[c]) : 0.f));
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(LT)
+    k_ln_bwd_row(const T *__restrict__ x, const T *__restrict__ gamma,
+                 const float *__restrict__ mean, const float *__restrict__ rstd, const T *dy,
+                 T *dx, long long rows, int C, float inv_c) {
+  __shared__ float sh[LT / 32];
+  for (long long p = blockIdx.x; p < rows; p += gridDim.x) {
+    const float mu = mean[p], r = rstd[p];
+    float c1 = 0.f, c2 = 0.f;
+    for (int c = threadIdx.x; c < C; c += LT) {
+      const float g = to_f<T>(dy[p * C + c]) * (gamma ? to_f<T>(gamma[c]) : 1.f);
+      c1 += g;
+      c2 = fmaf(g, (to_f<T>(x[p * C + c]) - mu) * r, c2);
+    }
+    c1 = cta_sum(c1, sh) * inv_c;
+    c2 = cta_sum(c2, sh) * inv_c;
+    for (int c = threadIdx.x; c < C; c += LT) {
+      const float g = to_f<T>(dy[p * C + c]) * (gamma ? to_f<T>(gamma[c]) : 1.f);
+      const float xh = (to_f<T>(x[p * C + c]) - mu) * r;
+      dx[p * C + c] = from_f<T>(r * (g - c1 - xh * c2));
+    }
+  }
+}
+
+// thread per channel over a slice of the rows
+template <typename T>
+__global__ void __launch_bounds__(LT)
+    k_ln_dparam_row(const T *__restrict__ x, const float *__restrict__ mean,
+                    const float *__restrict__ rstd, const T *__restrict__ dy,
+                    float *__restrict__ partial, long long rows, int C) {
+  const int c = blockIdx.x * LT + threadIdx.x;
+  if (c >= C) return;
+  float dg = 0.f, db = 0.f;
+  for (long long p = blockIdx.y; p < rows; p += gridDim.y) {
+    const float d = to_f<T>(dy[p * C + c]);
+    dg = fmaf(d, (to_f<T>(x[p * C + c]) - mean[p]) * rstd[p], dg);
+    db += d;
+  }
+  partial[((long long)blockIdx.y * C + c) * 2] = dg;
+  partial[((long long)blockIdx.y * C + c) * 2 + 1] = db;
+}
+
+#define FNO_DISPATCH_T(dtype, ...)                                \
+  do {                                                            \
+    if ((dtype) == DT_F32) {                                      \
+      using T = float;                                            \
+      __VA_ARGS__;                                                \
+    } else if ((dtype) == DT_F16) {                               \
+      using T = __half;                                           \
+      __VA_ARGS__;                                                \
+    } else {                                                      \
+      using T = __nv_bfloat16;                                    \
+      __VA_ARGS__;                                                \
+    }                                                             \
+  } while (0)
+
+unsigned capped(long long want, long long cap) {
+  return (unsigned)(want < 1 ? 1 : want < cap ? want : cap);
+}
+
+}  // namespace
+
+size_t ln_partial_bytes(int C) { return sizeof(float) * 2 * (size_t)C * kPartialCTAs; }
+
+cudaError_t launch_ln_fwd(const Launch &L, const NormShape &s, int dtype, const void *x,
+                          const void *gamma, const void *beta, void *y, float *mean,
+                          float *rstd) {
+  const long long points = s.outer * s.inner;
+  const float inv_c = 1.0f / (float)s.C;
+  launch_begin(L);
+  if (s.inner == 1) {
+    const unsigned grid = capped(points, 8LL * L.num_sms);
+    FNO_DISPATCH_T(dtype, k_ln_fwd_row<T><<<grid, LT, 0, L.stream>>>(
+                              (const T *)x, (const T *)gamma, (const T *)beta, (T *)y, mean, rstd,
+                              points, s.C, inv_c, s.eps));
+  } else {
+    const unsigned grid = capped((points + LT - 1) / LT, 8LL * L.num_sms);
+    FNO_DISPATCH_T(dtype, k_ln_fwd_point<T><<<grid, LT, 0, L.stream>>>(
+                              (const T *)x, (const T *)gamma, (const T *)beta, (T *)y, mean, rstd,
+                              points, s.C, s.inner, inv_c, s.eps));
+  }
+  const cudaError_t err = cudaGetLastError();
+  launch_end(L, "ln_fwd");
+  return err;
+}
+
+cudaError_t launch_ln_bwd(const Launch &L, const NormShape &s, int dtype, const void *x,
+                          const void *gamma, const float *mean, const float *rstd, const void *dy,
+                          void *dx, float *dgamma, float *dbeta, float *partial) {
+  const long long points = s.outer * s.inner;
+  const float inv_c = 1.0f / (float)s.C;
+  cudaError_t err;
+  // the parameter gradients first: dx may overwrite dy
+  if (dgamma || dbeta) {
+    int slices;
+    launch_begin(L);
+    if (s.inner == 1) {
+      slices = (int)capped((points + 15) / 16, kPartialCTAs);
+      const dim3 grid((s.C + LT - 1) / LT, slices);
+      FNO_DISPATCH_T(dtype, k_ln_dparam_row<T><<<grid, LT, 0, L.stream>>>(
+                                (const T *)x, mean, rstd, (const T *)dy, partial, points, s.C));
+    } else {
+      slices = (int)capped((points + 4 * LT - 1) / (4 * LT), kPartialCTAs);
+      const dim3 grid(s.C, slices);
+      FNO_DISPATCH_T(dtype, k_ln_dparam_point<T><<<grid, LT, 0, L.stream>>>(
+                                (const T *)x, mean, rstd, (const T *)dy, partial, points, s.C,
+                                s.inner));
+    }
+    err = cudaGetLastError();
+    launch_end(L, "ln_dparam");
+    if (err != cudaSuccess) return err;
+    err = launch_reduce_rows(L, partial, slices, 2LL * s.C, 0, s.C, 1, dgamma, dbeta);
+    if (err != cudaSuccess) return err;
+  }
+  launch_begin(L);
+  if (s.inner == 1) {
+    const unsigned grid = capped(points, 8LL * L.num_sms);
+    FNO_DISPATCH_T(dtype, k_ln_bwd_row<T><<<grid, LT, 0, L.stream>>>(
+                              (const T *)x, (const T *)gamma, mean, rstd, (const T *)dy, (T *)dx,
+                              points, s.C, inv_c));
+  } else {
+    const unsigned grid = capped((points + LT - 1) / LT, 8LL * L.num_sms);
+    FNO_DISPATCH_T(dtype, k_ln_bwd_point<T><<<grid, LT, 0, L.stream>>>(
+                              (const T *)x, (const T *)gamma, mean, rstd, (const T *)dy, (T *)dx,
+                              points, s.C, s.inner, inv_c));
+  }
+  err = cudaGetLastError();
+  launch_end(L, "ln_bwd");
+  return err;
+}
+
+}  // namespace fno

@@ -52,11 +52,18 @@ template <> __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16 
   *reinterpret_cast<uint2 *>(p) = u;
 }
 
-// n4 groups of four through 16-byte accesses, then the n - 4 n4 tail
+// n4 groups of four through 16-byte accesses, then the n - 4 n4 tail.  With
+// `clip` (norm, factor) the gradient scale takes the factor; a step skipped for
+// a norm that is not finite is the copy alone.
 template <typename T>
 __global__ void __launch_bounds__(AT)
     k_adam(long long n, long long n4, float *__restrict__ theta, float *__restrict__ m,
-           float *__restrict__ v, const float *__restrict__ g, T *__restrict__ out, AdamCoef c) {
+           float *__restrict__ v, const float *__restrict__ g, T *__restrict__ out, AdamCoef c,
+           const float *__restrict__ clip, bool skip_nonfinite) {
+  if (clip) {
+    if (skip_nonfinite && !(clip[0] <= 3.402823466e38f)) g = nullptr;
+    c.grad_scale *= clip[1];
+  }
   const long long stride = (long long)gridDim.x * AT;
   for (long long i = (long long)blockIdx.x * AT + threadIdx.x; i < n4; i += stride) {
     float4 th = reinterpret_cast<const float4 *>(theta)[i];
@@ -92,7 +99,8 @@ bool al8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7) == 0; }
 
 template <typename T>
 cudaError_t launch_adam_t(const Launch &L, long long n, float *theta, float *m, float *v,
-                          const float *g, void *out, const AdamCoef &c) {
+                          const float *g, void *out, const AdamCoef &c, const float *clip,
+                          bool skip_nonfinite) {
   // 16-byte groups need 16-byte aligned float arrays and an aligned 4-element copy
   const bool vec = al16(theta) && (!g || (al16(m) && al16(v) && al16(g))) &&
                    (!out || (sizeof(T) == 4 ? al16(out) : al8(out)));
@@ -103,19 +111,24 @@ cudaError_t launch_adam_t(const Launch &L, long long n, float *theta, float *m, 
   if (blocks > cap) blocks = cap;
   if (blocks < 1) blocks = 1;
   k_adam<T><<<(unsigned)blocks, AT, 0, L.stream>>>(n, n4, theta, m, v, g,
-                                                   reinterpret_cast<T *>(out), c);
+                                                   reinterpret_cast<T *>(out), c, clip,
+                                                   skip_nonfinite);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_adam(const Launch &L, long long n, float *theta, float *m, float *v,
-                        const float *g, void *out, int out_dtype, const AdamCoef &c) {
+                        const float *g, void *out, int out_dtype, const AdamCoef &c,
+                        const float *clip, bool skip_nonfinite) {
   launch_begin(L);
   cudaError_t err;
-  if (out_dtype == DT_F16) err = launch_adam_t<__half>(L, n, theta, m, v, g, out, c);
-  else if (out_dtype == DT_BF16) err = launch_adam_t<__nv_bfloat16>(L, n, theta, m, v, g, out, c);
-  else err = launch_adam_t<float>(L, n, theta, m, v, g, out, c);
+  if (out_dtype == DT_F16)
+    err = launch_adam_t<__half>(L, n, theta, m, v, g, out, c, clip, skip_nonfinite);
+  else if (out_dtype == DT_BF16)
+    err = launch_adam_t<__nv_bfloat16>(L, n, theta, m, v, g, out, c, clip, skip_nonfinite);
+  else
+    err = launch_adam_t<float>(L, n, theta, m, v, g, out, c, clip, skip_nonfinite);
   launch_end(L, g ? "adam" : "cast_params");
   return err;
 }

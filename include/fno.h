@@ -367,6 +367,84 @@ int fno_adam_step(int64_t n, float *theta, float *m, float *v, const float *grad
                   void *param_out, int out_dtype, int step, float lr, float beta1, float beta2,
                   float eps, float weight_decay, float grad_scale, fno_stream_t stream);
 
+/* Layer normalisation over the channel axis of x [outer][channels][inner] (Ba,
+ * Kiros and Hinton, "Layer Normalization", with the statistics per point):
+ *   mean = sum_c x / C,  var = sum_c (x - mean)^2 / C,  rstd = 1 / sqrt(var + eps)
+ *   y = (x - mean) rstd gamma + beta
+ * A batch of activations [B][C][N_0].. is outer = B, inner = prod N_j: each grid
+ * point is normalised over its channels.  inner = 1 is rows of channels
+ * [outer][C] (points with the features last).  All statistics are float32;
+ * y is rounded once to the storage dtype.  Values whose squares about the mean
+ * overflow float32 are outside its range.  A point that holds a NaN or an
+ * infinity becomes NaN throughout and touches no other point. */
+#define FNO_MAX_NORM_CHANNELS (1 << 20)
+typedef struct fno_norm_desc {
+  int dtype;     /* enum fno_dtype: x, y, dy, dx, gamma, beta */
+  int channels;  /* 1..FNO_MAX_NORM_CHANNELS */
+  int64_t outer; /* >= 1 */
+  int64_t inner; /* >= 1; outer * channels * inner <= 2^40 */
+  float eps;     /* > 0 */
+} fno_norm_desc;
+
+/* Workspace bytes of fno_layer_norm_bwd (the forward needs none); 0 for an
+ * invalid descriptor. */
+size_t fno_layer_norm_workspace_size(const fno_norm_desc *desc);
+
+/* y [outer][channels][inner] (storage dtype; may be x itself).  gamma, beta
+ * [channels] (storage dtype) may each be NULL: 1 and 0.  mean, rstd
+ * [outer][inner] (float32) are what the backward reads: both or neither. */
+int fno_layer_norm_fwd(const fno_norm_desc *desc, const void *x, const void *gamma,
+                       const void *beta, void *y, float *mean, float *rstd,
+                       fno_stream_t stream);
+
+/* Adjoint of fno_layer_norm_fwd, from x and the forward's mean and rstd.  With
+ * xh = (x - mean) rstd and g = dy gamma:
+ *   dx = rstd (g - sum_c g / C - xh sum_c g xh / C)
+ *   dgamma[c] = sum dy xh,  dbeta[c] = sum dy   (over every point)
+ * dx (storage dtype) may be dy itself, not x.  dgamma, dbeta [channels]
+ * (float32, overwritten) may each be NULL; with both NULL no workspace is
+ * needed.  The sums' order is fixed: equal calls give equal bits. */
+int fno_layer_norm_bwd(const fno_norm_desc *desc, const void *x, const void *gamma,
+                       const float *mean, const float *rstd, const void *dy, void *dx,
+                       float *dgamma, float *dbeta, void *ws, size_t ws_bytes,
+                       fno_stream_t stream);
+
+/* The global norm of many gradients and the factor that clips it (Pascanu,
+ * Mikolov and Bengio, "On the difficulty of training recurrent neural
+ * networks", section 3.2):
+ *   norm[0] = |grad_scale| sqrt(sum over all tensors of g^2)
+ *   norm[1] = 1 if norm[0] <= max_norm, else max_norm / norm[0]
+ * grads: host array of n_tensors device pointers, sizes: host array of their
+ * element counts (0 allowed: the tensor is passed over and its pointer not
+ * looked at), all in one dtype; both arrays are read before the call returns.
+ * Pointers need only their elements' alignment (16-byte aligned tensors are
+ * read fastest).  norm: device, two float32.  max_norm >= 0, INFINITY for the
+ * norm alone.  A norm of infinity gives the factor 0, a NaN gives NaN.  The
+ * sums are float64 in a fixed order, so squares beyond float32's range are
+ * held and equal calls give equal bits.  At most 2^40 elements in all. */
+size_t fno_grad_norm_workspace_size(int n_tensors);
+int fno_grad_norm(int n_tensors, const void *const *grads, const int64_t *sizes, int dtype,
+                  float grad_scale, float max_norm, float *norm, void *ws, size_t ws_bytes,
+                  fno_stream_t stream);
+
+/* fno_grad_norm, then out[i] = grads[i] * (grad_scale * norm[1]), rounded once to
+ * the dtype.  out: host array of device pointers; out[i] is grads[i] (in place;
+ * nothing is written where the multiplier is 1) or overlaps none of the
+ * tensors.  The tensors of one call must not overlap one another. */
+int fno_clip_grads(int n_tensors, const void *const *grads, void *const *out,
+                   const int64_t *sizes, int dtype, float grad_scale, float max_norm, float *norm,
+                   void *ws, size_t ws_bytes, fno_stream_t stream);
+
+/* fno_adam_step with the gradient multiplied by norm[1] as well (device, from
+ * fno_grad_norm on the same stream), so a clipped step writes no clipped
+ * gradients: g = grad * (grad_scale * norm[1]).  grad is required.
+ * skip_nonfinite != 0: where norm[0] is not finite (an overflow of half
+ * precision), theta, m and v stay as they are and param_out is theta's copy. */
+int fno_adam_step_clipped(int64_t n, float *theta, float *m, float *v, const float *grad,
+                          void *param_out, int out_dtype, int step, float lr, float beta1,
+                          float beta2, float eps, float weight_decay, float grad_scale,
+                          const float *norm, int skip_nonfinite, fno_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

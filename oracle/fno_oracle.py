@@ -261,6 +261,55 @@ def block_bwd(x, r, w, pre, xhat, dy, modes, flags: int = 0):
 
 
 # --------------------------------------------------------------------------
+# layer normalisation over the channel axis, gradient norm
+# --------------------------------------------------------------------------
+
+def layer_norm_fwd(x, gamma=None, beta=None, eps: float = 1e-5):
+    """``y = (x - mean) rstd gamma + beta`` over axis 1 of ``x [B, C, ...]``.
+
+    ``mean`` and ``rstd = 1 / sqrt(var + eps)`` are per point (the population
+    variance over the channels).  Returns ``(y, mean, rstd)``.
+    """
+    x = np.asarray(x, np.float64)
+    mean = x.sum(axis=1) / x.shape[1]
+    dev = x - mean[:, None]
+    rstd = 1.0 / np.sqrt((dev * dev).sum(axis=1) / x.shape[1] + eps)
+    y = dev * rstd[:, None]
+    if gamma is not None:
+        y = y * _bcast(gamma, x.ndim - 2)
+    if beta is not None:
+        y = y + _bcast(beta, x.ndim - 2)
+    return y, mean, rstd
+
+
+def layer_norm_bwd(x, gamma, mean, rstd, dy):
+    """Adjoint of :func:`layer_norm_fwd`: ``(dx, dgamma, dbeta)``.
+
+    With ``xh = (x - mean) rstd`` and ``g = dy gamma``, the chain rule through
+    the mean and the variance gives
+    ``dx = rstd (g - sum_c g / C - xh sum_c g xh / C)``.
+    """
+    x, dy = np.asarray(x, np.float64), np.asarray(dy, np.float64)
+    c = x.shape[1]
+    xh = (x - np.asarray(mean, np.float64)[:, None]) * np.asarray(rstd, np.float64)[:, None]
+    g = dy if gamma is None else dy * _bcast(gamma, x.ndim - 2)
+    dx = np.asarray(rstd, np.float64)[:, None] * (
+        g - g.sum(axis=1, keepdims=True) / c - xh * ((g * xh).sum(axis=1, keepdims=True) / c))
+    over = (0,) + tuple(range(2, x.ndim))
+    return dx, (dy * xh).sum(axis=over), dy.sum(axis=over)
+
+
+def grad_norm(grads, max_norm: float = np.inf, scale: float = 1.0):
+    """Global 2-norm of ``scale`` times every array, and the clipping factor
+    ``min(1, max_norm / norm)``."""
+    total = 0.0
+    for g in grads:
+        total += float(np.sum(np.abs(np.asarray(g, np.complex128)) ** 2))
+    norm = abs(scale) * np.sqrt(total)
+    return norm, (1.0 if norm <= max_norm else max_norm / norm)
+
+
+# --------------------------------------------------------------------------
 # network: lift -> L blocks -> projection ([MPFNO] "original FNO architecture")
 # --------------------------------------------------------------------------
 
