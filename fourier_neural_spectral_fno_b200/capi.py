@@ -31,6 +31,7 @@ DTYPE_CODE = {"f32": FNO_F32, "f16": FNO_F16, "bf16": FNO_BF16}
 
 FNO_TANH_PREACT = 1
 FNO_NO_ACT = 2
+FNO_LAYER_NORM = 4
 
 FNO_OP_SPECTRAL_FWD, FNO_OP_SPECTRAL_BWD, FNO_OP_BLOCK_FWD, FNO_OP_BLOCK_BWD = 0, 1, 2, 3
 FNO_OP_NET_FWD, FNO_OP_NET_BWD = 4, 5
@@ -95,7 +96,8 @@ _PARR = ctypes.c_void_p * FNO_MAX_LAYERS
 class Params(ctypes.Structure):
     _fields_ = [("P", ctypes.c_void_p), ("p", ctypes.c_void_p), ("R", _PARR), ("W", _PARR),
                 ("b", _PARR), ("Q1", ctypes.c_void_p), ("q1", ctypes.c_void_p),
-                ("Q2", ctypes.c_void_p), ("q2", ctypes.c_void_p)]
+                ("Q2", ctypes.c_void_p), ("q2", ctypes.c_void_p), ("ln_g", _PARR),
+                ("ln_b", _PARR)]
 
 
 class Grads(Params):
@@ -339,13 +341,14 @@ def fno_block_bwd(desc, x, R, W, pre_save, xhat_save, dy, dx, dR, dW, db, ws=Non
 
 
 def make_params(tensors: Dict[str, object]) -> Params:
-    """``Params`` from a dict of device tensors (``R``, ``W``, ``b`` are lists)."""
+    """``Params`` from a dict of device tensors (``R``, ``W``, ``b`` are lists, and
+    under FNO_LAYER_NORM ``ln_g``, ``ln_b``)."""
     p = Params()
     for key in ("P", "p", "Q1", "q1", "Q2", "q2"):
         setattr(p, key, _ptr(tensors[key]))
-    for key in ("R", "W", "b"):
+    for key in ("R", "W", "b", "ln_g", "ln_b"):
         arr = getattr(p, key)
-        for l, t in enumerate(tensors[key]):
+        for l, t in enumerate(tensors.get(key, ()) if key[:2] == "ln" else tensors[key]):
             arr[l] = _ptr(t)
     return p
 
@@ -354,9 +357,9 @@ def make_grads(tensors: Dict[str, object]) -> Grads:
     g = Grads()
     for key in ("P", "p", "Q1", "q1", "Q2", "q2"):
         setattr(g, key, _ptr(tensors[key]))
-    for key in ("R", "W", "b"):
+    for key in ("R", "W", "b", "ln_g", "ln_b"):
         arr = getattr(g, key)
-        for l, t in enumerate(tensors[key]):
+        for l, t in enumerate(tensors.get(key, ()) if key[:2] == "ln" else tensors[key]):
             arr[l] = _ptr(t)
     return g
 

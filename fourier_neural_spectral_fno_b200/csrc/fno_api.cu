@@ -408,7 +408,7 @@ int check_net(const fno_net_desc *d, Geom *g) {
   if (!d) return fail(FNO_ERR_INVALID_ARG, "descriptor is NULL");
   if (d->dtype < FNO_F32 || d->dtype > FNO_BF16)
     return fail(FNO_ERR_INVALID_ARG, "dtype %d unknown", d->dtype);
-  if (d->flags & ~(unsigned)(FNO_TANH_PREACT | FNO_NO_ACT))
+  if (d->flags & ~(unsigned)(FNO_TANH_PREACT | FNO_NO_ACT | FNO_LAYER_NORM))
     return fail(FNO_ERR_INVALID_ARG, "unknown flag bits 0x%x", d->flags);
   if (d->n_layers < 1 || d->n_layers > FNO_MAX_LAYERS)
     return fail(FNO_ERR_INVALID_ARG, "n_layers %d not in 1..%d", d->n_layers, FNO_MAX_LAYERS);
@@ -451,17 +451,25 @@ NetWs net_ws(const fno_net_desc *d, const Geom &g, int op) {
     size_t p = proj_bwd_partial_floats(d->width, d->hidden, d->out_channels);
     const size_t lift = (size_t)d->width * (d->in_channels + 1);
     if (lift > p) p = lift;
-    off += al(sizeof(float) * kPartialCTAs * p);
+    size_t bytes = sizeof(float) * kPartialCTAs * p;
+    if ((d->flags & FNO_LAYER_NORM) && ln_partial_bytes(d->width) > bytes)
+      bytes = ln_partial_bytes(d->width);
+    off += al(bytes);
   }
   w.total = off;
   return w;
 }
 
+// Per layer: the block's input, pre, xhat; with layer norm also the norm's
+// input (the previous block's output) and its statistics.
 struct SavesMap {
-  size_t act, xhat;
-  size_t x(int l) const { return (size_t)l * (2 * act + xhat); }
+  size_t act, xhat, stat;   // stat: 0 without layer norm
+  size_t x(int l) const { return (size_t)l * (2 * act + xhat + (stat ? act + 2 * stat : 0)); }
   size_t pre(int l) const { return x(l) + act; }
   size_t xh(int l) const { return x(l) + 2 * act; }
+  size_t v(int l) const { return stat ? xh(l) + xhat : x(l); }
+  size_t mean(int l) const { return v(l) + act; }
+  size_t rstd(int l) const { return mean(l) + stat; }
   size_t vlast(int L) const { return x(L); }
   size_t total(int L) const { return x(L) + act; }
 };
@@ -470,6 +478,7 @@ SavesMap saves_map(const fno_net_desc *d, const Geom &g) {
   SavesMap m;
   m.act = al(elsize(d->dtype) * (size_t)(g.B * d->width * g.N));
   m.xhat = al(sizeof(float2) * (size_t)(g.B * d->width * g.K));
+  m.stat = (d->flags & FNO_LAYER_NORM) ? al(sizeof(float) * (size_t)(g.B * g.N)) : 0;
   return m;
 }
 
@@ -858,6 +867,10 @@ int fno_forward(const fno_net_desc *desc, const void *a, const fno_params *param
     REQUIRE_PTR(params->R[l], "R[l]");
     REQUIRE_PTR(params->W[l], "W[l]");
     REQUIRE_PTR(params->b[l], "b[l]");
+    if (desc->flags & FNO_LAYER_NORM) {
+      REQUIRE_PTR(params->ln_g[l], "ln_g[l]");
+      REQUIRE_PTR(params->ln_b[l], "ln_b[l]");
+    }
   }
   REQUIRE_PTR(u, "u");
   OPTIONAL_PTR(saves, "saves");
@@ -869,15 +882,26 @@ int fno_forward(const fno_net_desc *desc, const void *a, const fno_params *param
   unsigned char *sv = (unsigned char *)saves;
   const SavesMap sm = saves_map(desc, g);
   const int nl = desc->n_layers;
-  auto act_buf = [&](int l) -> void * {  // input of block l (l == nl: projection input)
-    if (sv) return sv + (l < nl ? sm.x(l) : sm.vlast(nl));
+  const bool ln = desc->flags & FNO_LAYER_NORM;
+  auto act_buf = [&](int l) -> void * {  // output of block l - 1 (l == 0: lift)
+    if (sv) return sv + (l < nl ? sm.v(l) : sm.vlast(nl));
     return wsb + ((l & 1) ? w.act1 : w.act0);
   };
   FNO_TRY(launch_lift(L, g, desc->dtype, desc->in_channels, desc->width, a, params->P, params->p,
                       act_buf(0)),
           "lift");
+  const NormShape ns{g.B, g.N, desc->width, FNO_NET_NORM_EPS};
   for (int l = 0; l < nl; ++l) {
-    rc = run_forward(L, g, desc->dtype, desc->flags, desc->width, desc->width, act_buf(l),
+    void *in = act_buf(l);
+    if (ln) {   // in place where the forward saves nothing
+      void *v = in;
+      if (sv) in = sv + sm.x(l);
+      FNO_TRY(launch_ln_fwd(L, ns, desc->dtype, v, params->ln_g[l], params->ln_b[l], in,
+                            sv ? reinterpret_cast<float *>(sv + sm.mean(l)) : nullptr,
+                            sv ? reinterpret_cast<float *>(sv + sm.rstd(l)) : nullptr),
+              "layer norm");
+    }
+    rc = run_forward(L, g, desc->dtype, desc->flags, desc->width, desc->width, in,
                      params->R[l], params->W[l], params->b[l], act_buf(l + 1),
                      sv ? sv + sm.pre(l) : nullptr,
                      sv ? reinterpret_cast<float *>(sv + sm.xh(l)) : nullptr, wsb + w.block,
@@ -930,6 +954,11 @@ int fno_backward_ready(const fno_net_desc *desc, const void *a, const fno_params
     REQUIRE_PTR(grads->R[l], "dR[l]");
     REQUIRE_PTR(grads->W[l], "dW[l]");
     REQUIRE_PTR(grads->b[l], "db[l]");
+    if (desc->flags & FNO_LAYER_NORM) {
+      REQUIRE_PTR(params->ln_g[l], "ln_g[l]");
+      REQUIRE_PTR(grads->ln_g[l], "dln_g[l]");
+      REQUIRE_PTR(grads->ln_b[l], "dln_b[l]");
+    }
   }
   const NetWs w = net_ws(desc, g, FNO_OP_NET_BWD);
   if (ws_bytes < w.total) return fail(FNO_ERR_WORKSPACE, "workspace %zu B < %zu B", ws_bytes, w.total);
@@ -968,6 +997,13 @@ int fno_backward_ready(const fno_net_desc *desc, const void *a, const fno_params
                       sv + sm.pre(l), dv[(l + 1) & 1], dv[l & 1], grads->R[l], grads->W[l],
                       grads->b[l], wsb + w.block, true);
     if (rc) return rc;
+    if (desc->flags & FNO_LAYER_NORM)   // in place on the block's dx
+      FNO_TRY(launch_ln_bwd(L, NormShape{g.B, g.N, width, FNO_NET_NORM_EPS}, desc->dtype,
+                            sv + sm.v(l), params->ln_g[l],
+                            reinterpret_cast<const float *>(sv + sm.mean(l)),
+                            reinterpret_cast<const float *>(sv + sm.rstd(l)), dv[l & 1],
+                            dv[l & 1], grads->ln_g[l], grads->ln_b[l], partial),
+              "layer norm backward");
     if (ready) FNO_TRY(cudaEventRecord(ready[nl - l], L.stream), "recording a layer's ready event");
   }
   FNO_TRY(launch_lift_bwd(L, g, desc->dtype, desc->in_channels, width, a, dv[0], partial),

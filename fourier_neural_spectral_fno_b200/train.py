@@ -17,7 +17,9 @@ dtype, the all-reduce of the gradient (data parallelism over the batch: one
 collective per gradient group, started as soon as the backward has finished
 the group, so that it overlaps the backward of the earlier layers), then one
 fused ``fno_adam_step`` launch that updates the master copy
-and writes the next step's weights in the next step's dtype.
+and writes the next step's weights in the next step's dtype.  With gradient
+clipping the global norm is taken in front of it (``fno_grad_norm``), and the
+update reads the clipping factor on the device (``fno_adam_step_clipped``).
 
 Host logic only: every arithmetic step runs in ``libfno.so``; torch provides
 the buffers, the stream and ``torch.distributed``.
@@ -30,6 +32,7 @@ from typing import Dict, List, Optional, Sequence, Tuple
 import numpy as np
 
 from . import capi
+from .capi import FNO_LAYER_NORM
 
 STORAGE_DTYPES = ("f32", "f16", "bf16")
 ALIGN = 8   # elements per slot boundary: 16 bytes in every storage dtype
@@ -81,7 +84,8 @@ class PrecisionSchedule:
 class ParamLayout:
     """Slots of the network's parameters in one flat buffer.
 
-    Order: P, p, then per layer R[l], W[l], b[l], then Q1, q1, Q2, q2, with
+    Order: P, p, then per layer R[l], W[l], b[l] (with ``layer_norm`` also
+    ln_g[l], ln_b[l]), then Q1, q1, Q2, q2, with
     the shapes of ``fno_params`` (R as [width][width][|K|][2] (re, im)).  Every
     slot starts at a multiple of ``ALIGN`` elements; the gaps stay zero.  The
     parameters of each gradient group the backward finishes together (the
@@ -90,12 +94,15 @@ class ParamLayout:
     """
 
     def __init__(self, in_channels: int, width: int, hidden: int, out_channels: int,
-                 n_layers: int, n_modes: int):
+                 n_layers: int, n_modes: int, layer_norm: bool = False):
         self.n_layers = n_layers
+        self.layer_keys = ("R", "W", "b") + (("ln_g", "ln_b") if layer_norm else ())
         entries = [("P", None, (width, in_channels)), ("p", None, (width,))]
         for l in range(n_layers):
             entries += [("R", l, (width, width, n_modes, 2)), ("W", l, (width, width)),
                         ("b", l, (width,))]
+            if layer_norm:
+                entries += [("ln_g", l, (width,)), ("ln_b", l, (width,))]
         entries += [("Q1", None, (hidden, width)), ("q1", None, (hidden,)),
                     ("Q2", None, (out_channels, hidden)), ("q2", None, (out_channels,))]
         self.slots = []
@@ -125,8 +132,8 @@ class ParamLayout:
         return out
 
     def views(self, flat) -> Dict[str, object]:
-        """Per-parameter views of ``flat`` (lists for R, W, b)."""
-        out: Dict[str, object] = {"R": [], "W": [], "b": []}
+        """Per-parameter views of ``flat`` (lists for the layers' parameters)."""
+        out: Dict[str, object] = {k: [] for k in self.layer_keys}
         for key, layer, shape, off, size in self.slots:
             v = flat[off:off + size].view(*shape)
             if layer is None:
@@ -136,9 +143,13 @@ class ParamLayout:
         return out
 
     def pack(self, params: Dict[str, object], flat) -> None:
-        """Copy a parameter dict (NumPy or torch; complex R allowed) into ``flat``."""
+        """Copy a parameter dict (NumPy or torch; complex R allowed) into ``flat``.
+        Where the dict has no ``ln_g``, ``ln_b`` they start at 1 and 0."""
         import torch
         for key, layer, shape, off, size in self.slots:
+            if key in ("ln_g", "ln_b") and key not in params:
+                flat[off:off + size].fill_(1.0 if key == "ln_g" else 0.0)
+                continue
             val = params[key] if layer is None else params[key][layer]
             arr = np.asarray(val.detach().cpu().numpy() if isinstance(val, torch.Tensor) else val)
             if np.iscomplexobj(arr):
@@ -152,7 +163,7 @@ class ParamLayout:
     def unpack(self, flat) -> Dict[str, object]:
         """NumPy float64 parameter dict from ``flat`` (R complex)."""
         host = flat.detach().float().cpu().numpy().astype(np.float64)
-        out: Dict[str, object] = {"R": [], "W": [], "b": []}
+        out: Dict[str, object] = {k: [] for k in self.layer_keys}
         for key, layer, shape, off, size in self.slots:
             arr = host[off:off + size].reshape(shape)
             if key == "R":
@@ -172,14 +183,23 @@ class Trainer:
     ``process_group``: with more than one rank the flat gradient is summed by
     one all-reduce and the optimiser averages it (every rank holds an equal
     share of the global batch, so this is the gradient of the global-mean MSE).
+    ``flags``: the network's, FNO_LAYER_NORM among them (``params`` then may hold
+    ``ln_g``, ``ln_b``, one [width] per layer).
+    ``max_grad_norm``: clip the (averaged) gradient to this global norm.
+    ``skip_nonfinite``: a step whose gradient norm is not finite (an overflow of
+    half precision) changes no weight and no moment.  With either, ``grad_norm``
+    holds the last step's norm and clipping factor (float32 device tensor).
     """
 
     def __init__(self, grid: Sequence[int], modes: Sequence[int], in_channels: int, width: int,
                  params: Dict[str, object], schedule: PrecisionSchedule, hidden: int = 128,
                  out_channels: int = 1, n_layers: int = 4, flags: int = 0, lr: float = 1e-3,
                  betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8,
-                 weight_decay: float = 0.0, device=None, process_group=None):
+                 weight_decay: float = 0.0, device=None, process_group=None,
+                 max_grad_norm: Optional[float] = None, skip_nonfinite: bool = False):
         import torch
+        if max_grad_norm is not None and not max_grad_norm >= 0:
+            raise ValueError(f"max_grad_norm {max_grad_norm} < 0")
         self.grid, self.modes = tuple(int(n) for n in grid), tuple(int(m) for m in modes)
         self.in_channels, self.width, self.hidden = in_channels, width, hidden
         self.out_channels, self.n_layers, self.flags = out_channels, n_layers, flags
@@ -189,13 +209,17 @@ class Trainer:
             torch.device("cuda", torch.cuda.current_device())
         self.pg = process_group
         self.layout = ParamLayout(in_channels, width, hidden, out_channels, n_layers,
-                                  capi.num_modes(self.grid, self.modes))
+                                  capi.num_modes(self.grid, self.modes),
+                                  layer_norm=bool(flags & FNO_LAYER_NORM))
         n = self.layout.total
         self.master = torch.zeros(n, dtype=torch.float32, device=self.device)
         self.layout.pack(params, self.master)
         self.m = torch.zeros_like(self.master)
         self.v = torch.zeros_like(self.master)
         self.grad = torch.zeros_like(self.master)
+        self.max_grad_norm, self.skip_nonfinite = max_grad_norm, skip_nonfinite
+        self.grad_norm = None     # (norm, factor) of the last step, where it is taken
+        self._grad_list = self._norm_ws = None
         self.step_count = 0
         self.dtype: Optional[str] = None
         self.weights = None
@@ -246,7 +270,8 @@ class Trainer:
         return {"master": self.master.detach().cpu().clone(), "m": self.m.detach().cpu().clone(),
                 "v": self.v.detach().cpu().clone(), "step": self.step_count,
                 "phases": list(self.schedule.phases), "lr": self.lr, "betas": tuple(self.betas),
-                "eps": self.eps, "weight_decay": self.weight_decay, "slots": self.layout.total}
+                "eps": self.eps, "weight_decay": self.weight_decay, "slots": self.layout.total,
+                "max_grad_norm": self.max_grad_norm, "skip_nonfinite": self.skip_nonfinite}
 
     def load_state_dict(self, state: Dict[str, object]) -> None:
         """Resume from :meth:`state_dict` (same network shape)."""
@@ -259,6 +284,8 @@ class Trainer:
         self.schedule = PrecisionSchedule(state["phases"])
         self.lr, self.betas = float(state["lr"]), tuple(state["betas"])
         self.eps, self.weight_decay = float(state["eps"]), float(state["weight_decay"])
+        self.max_grad_norm = state.get("max_grad_norm", self.max_grad_norm)   # absent from
+        self.skip_nonfinite = bool(state.get("skip_nonfinite", self.skip_nonfinite))  # older ones
         self.dtype, self.weights = None, None     # the next step copies the master afresh
 
     def _allreduce_buckets(self) -> None:
@@ -276,6 +303,18 @@ class Trainer:
             with torch.cuda.stream(self._comm):
                 dist.all_reduce(self.grad[lo:hi], group=self.pg)
         torch.cuda.current_stream(self.device).wait_stream(self._comm)
+
+    def _take_norm(self, scale: float) -> None:
+        """The gradient's norm and clipping factor (the flat buffer's gaps are zero)."""
+        import torch
+        if self.grad_norm is None:
+            self.grad_norm = torch.zeros(2, dtype=torch.float32, device=self.device)
+            self._grad_list = capi.grad_list([self.grad])
+            self._norm_ws = torch.empty(capi.fno_grad_norm_workspace_size(self._grad_list),
+                                        dtype=torch.uint8, device=self.device)
+        limit = float("inf") if self.max_grad_norm is None else self.max_grad_norm
+        capi.fno_grad_norm(self._grad_list, limit, self.grad_norm, grad_scale=scale,
+                           ws=self._norm_ws)
 
     # ------------------------------------------------------------------- step
     def step(self, a, target):
@@ -319,7 +358,15 @@ class Trainer:
         nxt = self.schedule.dtype_at(self.step_count)
         out = w if nxt == dt else torch.empty(self.layout.total, dtype=torch_dtype(nxt),
                                               device=self.device)
-        capi.fno_adam_step(self.master, self.m, self.v, self.grad, out, self.step_count, self.lr,
-                           self.betas[0], self.betas[1], self.eps, self.weight_decay, scale)
+        if self.max_grad_norm is not None or self.skip_nonfinite:
+            self._take_norm(scale)
+            capi.fno_adam_step_clipped(self.master, self.m, self.v, self.grad, out,
+                                       self.step_count, self.lr, self.grad_norm, self.betas[0],
+                                       self.betas[1], self.eps, self.weight_decay, scale,
+                                       self.skip_nonfinite)
+        else:
+            capi.fno_adam_step(self.master, self.m, self.v, self.grad, out, self.step_count,
+                               self.lr, self.betas[0], self.betas[1], self.eps,
+                               self.weight_decay, scale)
         self.weights, self.dtype = out, nxt
         return b["loss"].clone()

@@ -81,7 +81,8 @@ enum fno_dtype { FNO_F32 = 0, FNO_F16 = 1, FNO_BF16 = 2 };
 
 enum fno_flags {
   FNO_TANH_PREACT = 1u, /* tanh on the spectral branch's input ([MPTRAIN]) */
-  FNO_NO_ACT = 2u       /* block output is pre (no GELU) */
+  FNO_NO_ACT = 2u,      /* block output is pre (no GELU) */
+  FNO_LAYER_NORM = 4u   /* network only: layer norm in front of every block */
 };
 
 enum fno_op {
@@ -114,7 +115,11 @@ typedef struct fno_block_desc {
 
 /* The network: v0 = P a + p (lift); v_{l+1} = block_l(v_l), l < n_layers,
  * every block width->width with the same modes and flags;
- * u = Q2 GELU(Q1 v_L + q1) + q2 (projection).  [MPFNO] "Proposed method". */
+ * u = Q2 GELU(Q1 v_L + q1) + q2 (projection).  [MPFNO] "Proposed method".
+ * Under FNO_LAYER_NORM v_{l+1} = block_l(LN_l(v_l)): each point normalised over
+ * its channels (fno_layer_norm_fwd with eps = FNO_NET_NORM_EPS) with the
+ * layer's own ln_g and ln_b, so a block's scale does not grow with depth. */
+#define FNO_NET_NORM_EPS 1e-5f
 typedef struct fno_net_desc {
   int ndim;
   int dtype;
@@ -138,6 +143,8 @@ typedef struct fno_params {
   const void *W[FNO_MAX_LAYERS];
   const void *b[FNO_MAX_LAYERS];
   const void *Q1, *q1, *Q2, *q2;
+  const void *ln_g[FNO_MAX_LAYERS]; /* [width]; read under FNO_LAYER_NORM alone */
+  const void *ln_b[FNO_MAX_LAYERS];
 } fno_params;
 
 /* Parameter gradients (device, float32), same shapes as fno_params. */
@@ -147,6 +154,8 @@ typedef struct fno_grads {
   float *W[FNO_MAX_LAYERS];
   float *b[FNO_MAX_LAYERS];
   float *Q1, *q1, *Q2, *q2;
+  float *ln_g[FNO_MAX_LAYERS]; /* written under FNO_LAYER_NORM alone */
+  float *ln_b[FNO_MAX_LAYERS];
 } fno_grads;
 
 /* Thread-local message of the last failing call on this thread ("" if none). */
@@ -330,7 +339,8 @@ int fno_backward(const fno_net_desc *desc, const void *a, const fno_params *para
  * the groups in this order and records ready[j] (cudaEventRecord on `stream`)
  * right after group j's last kernel:
  *   ready[0]                 dQ1, dq1, dQ2, dq2 (projection)
- *   ready[1 + j], j < L      dR, dW, db of layer L - 1 - j (L = n_layers)
+ *   ready[1 + j], j < L      dR, dW, db (and dln_g, dln_b) of layer L - 1 - j
+ *                            (L = n_layers)
  *   ready[L + 1]             dP, dp (lift)
  * The events belong to the caller (created by it, any flags); n_ready must be
  * n_layers + 2.  A caller that makes a second stream wait on ready[j] can start

@@ -7,4 +7,4 @@ from .fno_oracle import (axis_wavenumbers, kept_shape, num_modes, mode_weights,
                          round_to_storage, adam_update, dtype_at, train,
                          cp_weights, spectral_conv_fwd_cp, cp_factor_grads,
                          spectral_conv_bwd_cp, layer_norm_fwd, layer_norm_bwd, grad_norm,
-                         TANH_PREACT, NO_ACT)
+                         TANH_PREACT, NO_ACT, LAYER_NORM)

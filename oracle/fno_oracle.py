@@ -64,6 +64,7 @@ import numpy as np
 
 TANH_PREACT = 1
 NO_ACT = 2
+LAYER_NORM = 4     # network only: layer norm in front of every block
 
 _SQRT1_2 = 1.0 / math.sqrt(2.0)
 _INV_SQRT_2PI = 1.0 / math.sqrt(2.0 * math.pi)
@@ -331,14 +332,20 @@ def forward(a, params, modes, flags: int = 0, save: bool = False):
     """``v_0 = P a + p``; ``v_{l+1} = block_l(v_l)``; ``u = Q2 GELU(Q1 v_L + q1) + q2``.
 
     ``params`` is a dict with ``P, p, R (list), W (list), b (list), Q1, q1, Q2, q2``.
+    Under LAYER_NORM each block reads its input normalised over the channels with
+    ``ln_g[l]``, ``ln_b[l]`` (:func:`layer_norm_fwd`).
     Returns ``u`` or ``(u, saves)`` with the per-layer block inputs, pre-activations,
     spectra and the projection's hidden pre-activation.
     """
     a = np.asarray(a, np.float64)
     d = a.ndim - 2
     v = lift(a, params["P"], params["p"])
-    xs, pres, xhats = [], [], []
-    for r, w, bias in zip(params["R"], params["W"], params["b"]):
+    xs, pres, xhats, norms = [], [], [], []
+    for l, (r, w, bias) in enumerate(zip(params["R"], params["W"], params["b"])):
+        if flags & LAYER_NORM:
+            raw = v
+            v, mean, rstd = layer_norm_fwd(raw, params["ln_g"][l], params["ln_b"][l])
+            norms.append((raw, mean, rstd))
         xs.append(v)
         v, pre, xhat = block_fwd(v, r, w, bias, modes, flags)
         pres.append(pre)
@@ -347,7 +354,7 @@ def forward(a, params, modes, flags: int = 0, save: bool = False):
     u = projection(v, params["Q1"], params["q1"], params["Q2"], params["q2"])
     if not save:
         return u
-    return u, {"x": xs, "pre": pres, "xhat": xhats, "v_last": v, "h": h}
+    return u, {"x": xs, "pre": pres, "xhat": xhats, "v_last": v, "h": h, "norm": norms}
 
 
 def backward(a, params, saves, du, modes, flags: int = 0):
@@ -367,10 +374,16 @@ def backward(a, params, saves, du, modes, flags: int = 0):
     dv = _pointwise(np.asarray(params["Q1"], np.float64).T, dh)
     n_layers = len(params["R"])
     d_r, d_w, d_b = [None] * n_layers, [None] * n_layers, [None] * n_layers
+    d_g, d_h = [None] * n_layers, [None] * n_layers
     for l in range(n_layers - 1, -1, -1):
         dv, d_r[l], d_w[l], d_b[l] = block_bwd(
             saves["x"][l], params["R"][l], params["W"][l], saves["pre"][l],
             saves["xhat"][l], dv, modes, flags)
+        if flags & LAYER_NORM:
+            raw, mean, rstd = saves["norm"][l]
+            dv, d_g[l], d_h[l] = layer_norm_bwd(raw, params["ln_g"][l], mean, rstd, dv)
+    if flags & LAYER_NORM:
+        grads["ln_g"], grads["ln_b"] = d_g, d_h
     grads["R"], grads["W"], grads["b"] = d_r, d_w, d_b
     grads["P"] = _outer_sum(dv, a)
     grads["p"] = dv.sum(axis=(0,) + spatial)
@@ -436,13 +449,18 @@ def dtype_at(phases, step: int) -> str:
 
 _PARAM_KEYS = ("P", "p", "Q1", "q1", "Q2", "q2")
 _LAYER_KEYS = ("R", "W", "b")
+_NORM_KEYS = ("ln_g", "ln_b")
+
+
+def _layer_keys(params):
+    return _LAYER_KEYS + tuple(k for k in _NORM_KEYS if k in params)
 
 
 def _map_params(fn, *trees):
     out = {}
     for key in _PARAM_KEYS:
         out[key] = fn(*[t[key] for t in trees])
-    for key in _LAYER_KEYS:
+    for key in _layer_keys(trees[0]):
         out[key] = [fn(*xs) for xs in zip(*[t[key] for t in trees])]
     return out
 
@@ -455,13 +473,15 @@ def _round_param(x, dtype):
 
 
 def train(a, target, params, modes, phases, steps: int, lr: float, beta1: float = 0.9,
-          beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.0, flags: int = 0):
+          beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.0, flags: int = 0,
+          max_grad_norm: float = np.inf):
     """``steps`` Adam steps of the network on one batch under a precision schedule.
 
     Step ``t`` (0-based) reads the master parameters and the inputs rounded to
     ``dtype_at(phases, t)``, takes the MSE gradient of :func:`forward` there and
     applies :func:`adam_update` (step number ``t + 1``) to the float64 master
-    copy.  Complex weights are updated as (re, im) pairs.  Returns
+    copy.  Complex weights are updated as (re, im) pairs.  Gradients are clipped
+    to the global norm ``max_grad_norm`` (:func:`grad_norm`).  Returns
     ``(master params, losses)``.
     """
     master = _map_params(lambda x: np.array(x, dtype=np.complex128 if np.iscomplexobj(x)
@@ -477,8 +497,11 @@ def train(a, target, params, modes, phases, steps: int, lr: float, beta1: float 
         loss, du = mse(u, t_q)
         losses.append(loss)
         grads = backward(a_q, q, saves, du, modes, flags)
+        every = [grads[k] for k in _PARAM_KEYS] + [x for k in _layer_keys(master) for x in grads[k]]
+        _, factor = grad_norm(every, max_grad_norm)
 
-        def upd(th, mm, vv, gg, step=t + 1):
+        def upd(th, mm, vv, gg, step=t + 1, factor=factor):
+            gg = gg * factor
             if np.iscomplexobj(th):   # real and imaginary parts are separate parameters
                 re = adam_update(th.real, mm.real, vv.real, np.real(gg), step, lr, beta1, beta2,
                                  eps, weight_decay)
@@ -490,7 +513,7 @@ def train(a, target, params, modes, phases, steps: int, lr: float, beta1: float 
         new = {}
         for key in _PARAM_KEYS:
             new[key] = upd(master[key], mom[key], vel[key], grads[key])
-        for key in _LAYER_KEYS:
+        for key in _layer_keys(master):
             new[key] = [upd(*xs) for xs in zip(master[key], mom[key], vel[key], grads[key])]
         master = {k: ([x[0] for x in v] if isinstance(v, list) else v[0]) for k, v in new.items()}
         mom = {k: ([x[1] for x in v] if isinstance(v, list) else v[1]) for k, v in new.items()}
