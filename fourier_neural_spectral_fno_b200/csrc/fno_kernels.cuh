@@ -276,6 +276,7 @@ struct NormShape {
   int C;
   float eps;
 };
+constexpr int kLnParts = 592;   // most CTAs that write partial parameter gradients
 size_t ln_partial_bytes(int C);
 // gamma, beta may be NULL (1, 0); mean, rstd [outer][inner] both or neither; y may be x
 cudaError_t launch_ln_fwd(const Launch &L, const NormShape &s, int dtype, const void *x,

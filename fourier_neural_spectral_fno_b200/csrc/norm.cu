@@ -9,8 +9,7 @@
 // sweep over the values, which also gives e = mean(x - m0), the rounding of m0:
 // mean = m0 + e, var = mean((x - m0)^2) - e^2, xh = ((x - m0) - e) rstd, so a
 // common offset far above the spread costs no more than the offset's own storage.
-#include "fno_common.cuh"
-#include "fno_kernels.cuh"
+#include "norm_common.cuh"
 
 namespace fno {
 
@@ -59,8 +58,7 @@ __global__ void __launch_bounds__(LT)
       q = fmaf(d, d, q);
     }
     e *= inv_c;
-    const float var = fmaxf(fmaf(-e, e, q * inv_c), 0.f);
-    const float r = 1.0f / sqrtf((q != q ? q : var) + eps);
+    const float r = ln_rstd(q * inv_c, e, eps);
     if (mean) {
       mean[p] = m0 + e;
       rstd[p] = r;
@@ -142,8 +140,7 @@ __global__ void __launch_bounds__(LT)
     }
     e = cta_sum(e, sh) * inv_c;
     q = cta_sum(q, sh);
-    const float var = fmaxf(fmaf(-e, e, q * inv_c), 0.f);
-    const float r = 1.0f / sqrtf((q != q ? q : var) + eps);
+    const float r = ln_rstd(q * inv_c, e, eps);
     if (mean && threadIdx.x == 0) {
       mean[p] = m0 + e;
       rstd[p] = r;
@@ -197,31 +194,21 @@ __global__ void __launch_bounds__(LT)
   partial[((long long)blockIdx.y * C + c) * 2 + 1] = db;
 }
 
-#define FNO_DISPATCH_T(dtype, ...)                                \
-  do {                                                            \
-    if ((dtype) == DT_F32) {                                      \
-      using T = float;                                            \
-      __VA_ARGS__;                                                \
-    } else if ((dtype) == DT_F16) {                               \
-      using T = __half;                                           \
-      __VA_ARGS__;                                                \
-    } else {                                                      \
-      using T = __nv_bfloat16;                                    \
-      __VA_ARGS__;                                                \
-    }                                                             \
-  } while (0)
-
 unsigned capped(long long want, long long cap) {
   return (unsigned)(want < 1 ? 1 : want < cap ? want : cap);
 }
 
 }  // namespace
 
-size_t ln_partial_bytes(int C) { return sizeof(float) * 2 * (size_t)C * kPartialCTAs; }
+size_t ln_partial_bytes(int C) { return sizeof(float) * 2 * (size_t)C * kLnParts; }
 
 cudaError_t launch_ln_fwd(const Launch &L, const NormShape &s, int dtype, const void *x,
                           const void *gamma, const void *beta, void *y, float *mean,
                           float *rstd) {
+  if (ln_pipe_supported(s, dtype, false))
+    return launch_ln_pipe_fwd(L, s, dtype, x, gamma, beta, y, mean, rstd);
+  if (ln_grid_supported(s, dtype, false))
+    return launch_ln_grid_fwd(L, s, dtype, x, gamma, beta, y, mean, rstd);
   const long long points = s.outer * s.inner;
   const float inv_c = 1.0f / (float)s.C;
   launch_begin(L);
@@ -247,17 +234,31 @@ cudaError_t launch_ln_bwd(const Launch &L, const NormShape &s, int dtype, const 
   const long long points = s.outer * s.inner;
   const float inv_c = 1.0f / (float)s.C;
   cudaError_t err;
+  int nparts = 0;
+  const bool params = dgamma || dbeta;
+  if (ln_pipe_supported(s, dtype, true)) {
+    err = launch_ln_pipe_bwd(L, s, dtype, x, gamma, mean, rstd, dy, dx,
+                             params ? partial : nullptr, &nparts);
+    if (err != cudaSuccess || !params) return err;
+    return launch_reduce_rows(L, partial, nparts, 2LL * s.C, 0, s.C, 1, dgamma, dbeta);
+  }
+  if (ln_grid_supported(s, dtype, true)) {
+    err = launch_ln_grid_bwd(L, s, dtype, x, gamma, mean, rstd, dy, dx,
+                             params ? partial : nullptr, &nparts);
+    if (err != cudaSuccess || !params) return err;
+    return launch_reduce_rows(L, partial, nparts, 2LL * s.C, 0, s.C, 1, dgamma, dbeta);
+  }
   // the parameter gradients first: dx may overwrite dy
   if (dgamma || dbeta) {
     int slices;
     launch_begin(L);
     if (s.inner == 1) {
-      slices = (int)capped((points + 15) / 16, kPartialCTAs);
+      slices = (int)capped((points + 15) / 16, kLnParts);
       const dim3 grid((s.C + LT - 1) / LT, slices);
       FNO_DISPATCH_T(dtype, k_ln_dparam_row<T><<<grid, LT, 0, L.stream>>>(
                                 (const T *)x, mean, rstd, (const T *)dy, partial, points, s.C));
     } else {
-      slices = (int)capped((points + 4 * LT - 1) / (4 * LT), kPartialCTAs);
+      slices = (int)capped((points + 4 * LT - 1) / (4 * LT), kLnParts);
       const dim3 grid(s.C, slices);
       FNO_DISPATCH_T(dtype, k_ln_dparam_point<T><<<grid, LT, 0, L.stream>>>(
                                 (const T *)x, mean, rstd, (const T *)dy, partial, points, s.C,

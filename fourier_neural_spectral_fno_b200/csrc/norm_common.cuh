@@ -1,0 +1,167 @@
+// Helpers shared by the layer norm kernels.
+#pragma once
+
+#include "fno_common.cuh"
+#include "fno_kernels.cuh"
+
+namespace fno {
+
+// the two values of a four-byte word of a 16-bit type
+template <typename T> __device__ __forceinline__ void word_get(unsigned w, float &a, float &b);
+template <> __device__ __forceinline__ void word_get<__half>(unsigned w, float &a, float &b) {
+  const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+  a = t.x;
+  b = t.y;
+}
+template <>
+__device__ __forceinline__ void word_get<__nv_bfloat16>(unsigned w, float &a, float &b) {
+  a = __uint_as_float(w << 16);
+  b = __uint_as_float(w & 0xffff0000u);
+}
+template <typename T> __device__ __forceinline__ unsigned word_set(float a, float b);
+template <> __device__ __forceinline__ unsigned word_set<__half>(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const unsigned *>(&h);
+}
+template <> __device__ __forceinline__ unsigned word_set<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const unsigned *>(&h);
+}
+
+// V consecutive values of the storage type as one memory access of V sizeof(T)
+// bytes (16, or one element).  keep() hides the values' origin from the compiler:
+// a later sweep converts the packed registers again instead of holding the
+// converted ones, which for 16-bit types take twice as many.
+template <typename T, int V> struct Pack;
+template <> struct Pack<float, 4> {
+  float4 r;
+  __device__ __forceinline__ void keep() {
+    asm volatile("" : "+f"(r.x), "+f"(r.y), "+f"(r.z), "+f"(r.w));
+  }
+  __device__ __forceinline__ void zero() { r = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float *f) const { f[0] = r.x; f[1] = r.y; f[2] = r.z; f[3] = r.w; }
+  __device__ __forceinline__ void set(const float *f) { r = make_float4(f[0], f[1], f[2], f[3]); }
+};
+template <> struct Pack<__half, 8> {
+  uint4 r;
+  __device__ __forceinline__ void keep() {
+    asm volatile("" : "+r"(r.x), "+r"(r.y), "+r"(r.z), "+r"(r.w));
+  }
+  __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float *f) const {
+    const unsigned w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+      f[2 * i] = t.x;
+      f[2 * i + 1] = t.y;
+    }
+  }
+  __device__ __forceinline__ void set(const float *f) {
+    unsigned w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const unsigned *>(&h);
+    }
+    r = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+template <> struct Pack<__nv_bfloat16, 8> {
+  uint4 r;
+  __device__ __forceinline__ void keep() {
+    asm volatile("" : "+r"(r.x), "+r"(r.y), "+r"(r.z), "+r"(r.w));
+  }
+  __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
+  // a bfloat16 is the upper half of the float32 of the same value
+  __device__ __forceinline__ void get(float *f) const {
+    const unsigned w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  __device__ __forceinline__ void set(const float *f) {
+    unsigned w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const unsigned *>(&h);
+    }
+    r = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+template <typename T> struct Pack<T, 4> {   // 16-bit types: 8 bytes
+  uint2 r;
+  __device__ __forceinline__ void keep() { asm volatile("" : "+r"(r.x), "+r"(r.y)); }
+  __device__ __forceinline__ void zero() { r = make_uint2(0, 0); }
+  __device__ __forceinline__ void get(float *f) const {
+    word_get<T>(r.x, f[0], f[1]);
+    word_get<T>(r.y, f[2], f[3]);
+  }
+  __device__ __forceinline__ void set(const float *f) {
+    r = make_uint2(word_set<T>(f[0], f[1]), word_set<T>(f[2], f[3]));
+  }
+};
+template <typename T> struct Pack<T, 1> {
+  T r;
+  __device__ __forceinline__ void keep() {}
+  __device__ __forceinline__ void zero() { r = from_f<T>(0.f); }
+  __device__ __forceinline__ void get(float *f) const { f[0] = to_f<T>(r); }
+  __device__ __forceinline__ void set(const float *f) { r = from_f<T>(f[0]); }
+};
+
+// hides a value's origin, so that what depends on it is computed again (inside a
+// loop: in each round) rather than held in registers: multiples of a channel's
+// stride, above all
+__device__ __forceinline__ long long again(long long v) {
+  asm volatile("" : "+l"(v));
+  return v;
+}
+
+template <typename T> struct VecOf { static constexpr int N = 16 / sizeof(T); };
+
+// 1 / sqrt(var + eps) with var = q / C - e^2 from the deviations about a first
+// mean: never below zero by rounding, and a NaN stays one
+__device__ __forceinline__ float ln_rstd(float q_mean, float e, float eps) {
+  const float var = fmaf(-e, e, q_mean);
+  return 1.0f / sqrtf((var < 0.f ? 0.f : var) + eps);
+}
+
+#define FNO_DISPATCH_T(dtype, ...)                                \
+  do {                                                            \
+    if ((dtype) == DT_F32) {                                      \
+      using T = float;                                            \
+      __VA_ARGS__;                                                \
+    } else if ((dtype) == DT_F16) {                               \
+      using T = __half;                                           \
+      __VA_ARGS__;                                                \
+    } else {                                                      \
+      using T = __nv_bfloat16;                                    \
+      __VA_ARGS__;                                                \
+    }                                                             \
+  } while (0)
+
+// ---- per-layout kernels -----------------------------------------------------
+// grid layout (inner > 1), values held in registers (norm_grid.cu)
+bool ln_grid_supported(const NormShape &s, int dtype, bool bwd);
+cudaError_t launch_ln_grid_fwd(const Launch &L, const NormShape &s, int dtype, const void *x,
+                               const void *gamma, const void *beta, void *y, float *mean,
+                               float *rstd);
+// writes dx and, unless partial is NULL, *nparts rows of [C][2] (dgamma, dbeta)
+// partial sums
+cudaError_t launch_ln_grid_bwd(const Launch &L, const NormShape &s, int dtype, const void *x,
+                               const void *gamma, const float *mean, const float *rstd,
+                               const void *dy, void *dx, float *partial, int *nparts);
+
+// the same as a TMA pipeline, at most 64 channels (norm_pipe.cu)
+bool ln_pipe_supported(const NormShape &s, int dtype, bool bwd);
+cudaError_t launch_ln_pipe_fwd(const Launch &L, const NormShape &s, int dtype, const void *x,
+                               const void *gamma, const void *beta, void *y, float *mean,
+                               float *rstd);
+cudaError_t launch_ln_pipe_bwd(const Launch &L, const NormShape &s, int dtype, const void *x,
+                               const void *gamma, const float *mean, const float *rstd,
+                               const void *dy, void *dx, float *partial, int *nparts);
+
+}  // namespace fno

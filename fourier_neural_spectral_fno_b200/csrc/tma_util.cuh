@@ -8,7 +8,8 @@
 //  * the innermost box extent times the element size is a multiple of 16
 //    bytes, and so is every innermost start coordinate times the element size;
 //  * destinations in shared memory are 128-byte aligned;
-//  * loads only (no multicast, no stores or reductions through TMA).
+//  * no multicast and no reductions; a store's start coordinates are never
+//    negative, and what lies beyond the tensor is not written.
 #pragma once
 
 #include <cuda.h>
@@ -42,6 +43,29 @@ __device__ __forceinline__ void load_bulk(void *dst, const void *src, uint32_t b
           tc::smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(tc::smem_u32(mbar))
       : "memory");
+}
+
+// 4-D tiled store of one box from shared memory (written through
+// fence.proxy.async by its writers), completed through the issuing thread's bulk
+// groups: store_commit closes a group, store_wait_read<N> returns when all but
+// the newest N groups have read their shared memory, store_wait_all when all are
+// written.
+__device__ __forceinline__ void store_4d(const CUtensorMap *map, const void *src, int c0, int c1,
+                                         int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(tc::smem_u32(src))
+      : "memory");
+}
+__device__ __forceinline__ void store_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+template <int N> __device__ __forceinline__ void store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void store_wait_all() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {

@@ -128,6 +128,78 @@ def test_layer_norm_matches_oracle(shape, dtype):
     assert np.array_equal(_host(xd), x) and np.array_equal(_host(dyd), dy)
 
 
+def _check_large(got, ref, tol, what):
+    """On the device: |got - ref| <= tol everywhere."""
+    worst = ((got.double() - ref).abs() - tol).max().item()
+    assert worst <= 0, f"{what}: {worst} beyond its tolerance"
+
+
+# sizes from a million values on, where the copies run as pipelines: every
+# channel count they round up to and odd ones between, rows that end inside a
+# tile, one sample and many, one tile per sample
+LARGE = [(3, 5, 281000), (17, 8, 33000), (2, 13, 163848), (5, 16, 53000), (1, 17, 250008),
+         (3, 20, 70008), (4, 23, 46000), (7, 24, 25000), (2, 31, 68008), (540, 32, 256),
+         (3, 45, 31512), (2, 48, 44000), (3, 61, 23000), (2, 64, 33000), (130, 64, 520)]
+
+
+@pytest.mark.parametrize("shape", LARGE, ids=str)
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_layer_norm_large_matches_float64(shape, dtype):
+    """The formulas in float64 torch operations, with the tolerances above; guard
+    bands, and dx over dy giving the same bits."""
+    import torch
+    outer, C, inner = shape
+    g = torch.Generator(device="cuda").manual_seed(13)
+    dt = torch_dtype(dtype)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    x = (rnd(outer, C, inner) * torch.exp(0.5 * rnd(1, C, 1)) + 0.7 * rnd(1, C, 1)).to(dt)
+    gamma, beta = (1 + 0.2 * rnd(C)).to(dt), (0.2 * rnd(C)).to(dt)
+    dy = (0.3 * rnd(outer, C, inner)).to(dt)
+    d = capi.layer_norm_desc(outer, C, inner, dtype, EPS)
+    y, ybuf = _bands(x.shape, dtype)
+    mean, mbuf = _bands((outer, inner), "f32")
+    rstd, rbuf = _bands((outer, inner), "f32")
+    capi.fno_layer_norm_fwd(d, x, gamma, beta, y, mean, rstd)
+    assert _untouched(ybuf, x.numel())
+    assert _untouched(mbuf, mean.numel()) and _untouched(rbuf, mean.numel())
+    x6, ga, be = x.double(), gamma.double()[:, None], beta.double()[:, None]
+    rm = x6.mean(1)
+    rr = 1 / ((x6 - rm[:, None]).square().mean(1) + EPS).sqrt()
+    xh = (x6 - rm[:, None]) * rr[:, None]
+    ry = xh * ga + be
+    tol = (2 * C + 16) * U * (1 + xh.abs()) * ga.abs() + 4 * U * ry.abs()
+    _check_large(y, ry, tol + HALF[dtype] * (ry.abs() + tol) + TINY[dtype], "y")
+    _check_large(mean, rm, (C + 4) * U * x6.abs().mean(1), "mean")
+    _check_large(rstd, rr, (C + 16) * U * rr, "rstd")
+    y2 = torch.empty_like(x)
+    capi.fno_layer_norm_fwd(d, x, gamma, beta, y2)
+    assert torch.equal(y2, y)
+    same = x.clone()
+    capi.fno_layer_norm_fwd(d, same, gamma, beta, same)
+    assert torch.equal(same, y)
+
+    dx, dxbuf = _bands(x.shape, dtype)
+    dg, db = torch.empty(C, device="cuda"), torch.empty(C, device="cuda")
+    capi.fno_layer_norm_bwd(d, x, gamma, mean, rstd, dy, dx, dg, db)
+    assert _untouched(dxbuf, x.numel())
+    mu, r, dy6 = mean.double()[:, None], rstd.double()[:, None], dy.double()
+    xh = (x6 - mu) * r
+    gg = dy6 * ga
+    rdx = r * (gg - gg.mean(1, keepdim=True) - xh * (gg * xh).mean(1, keepdim=True))
+    tol = r * (C + 16) * U * (gg.abs() + gg.abs().mean(1, keepdim=True)
+                              + xh.abs() * (gg * xh).abs().mean(1, keepdim=True))
+    _check_large(dx, rdx, tol + HALF[dtype] * (rdx.abs() + tol) + TINY[dtype], "dx")
+    for got, each, name in ((dg, dy6 * xh, "dgamma"), (db, dy6, "dbeta")):
+        _check_large(got, each.sum((0, 2)), (4096 + 68) * U * each.abs().sum((0, 2)), name)
+    dg2, db2, dx2 = torch.empty_like(dg), torch.empty_like(db), torch.empty_like(x)
+    capi.fno_layer_norm_bwd(d, x, gamma, mean, rstd, dy, dx2, None, db2)
+    assert torch.equal(dx2, dx) and torch.equal(db2, db)
+    capi.fno_layer_norm_bwd(d, x, gamma, mean, rstd, dy, dx2)
+    assert torch.equal(dx2, dx)
+    capi.fno_layer_norm_bwd(d, x, gamma, mean, rstd, dy, dy, dg2, db2)
+    assert torch.equal(dy, dx) and torch.equal(dg2, dg) and torch.equal(db2, db)
+
+
 @pytest.mark.parametrize("shape", [(2, 20, 96), (3, 20, 35), (6, 40, 1), (3, 41, 1), (2, 1100, 5),
                                    (2, 200, 12), (1, 33001, 1)], ids=str)
 def test_layer_norm_optional_arguments_and_in_place(shape):
@@ -251,7 +323,8 @@ def test_layer_norm_gradient_by_differences():
             assert abs(num - _host(grad)[idx]) <= 3e-3 * max(1.0, abs(num))
 
 
-@pytest.mark.parametrize("shape", [(4, 20, 4096), (3, 64, 4099), (500, 96, 1), (4, 2050, 1)], ids=str)
+@pytest.mark.parametrize("shape", [(4, 20, 4096), (3, 64, 4099), (500, 96, 1), (4, 2050, 1),
+                                   (3, 64, 24008), (2, 20, 120000)], ids=str)
 def test_layer_norm_on_streams_and_in_a_graph(shape):
     """Two calls at once on two streams with their own workspaces, and a captured
     forward + backward replayed on new inputs: the same bits as plain calls."""
