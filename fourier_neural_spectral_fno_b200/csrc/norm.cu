@@ -207,6 +207,8 @@ cudaError_t launch_ln_fwd(const Launch &L, const NormShape &s, int dtype, const 
                           float *rstd) {
   if (ln_pipe_supported(s, dtype, false))
     return launch_ln_pipe_fwd(L, s, dtype, x, gamma, beta, y, mean, rstd);
+  if (ln_rows_supported(s, dtype, false))
+    return launch_ln_rows_fwd(L, s, dtype, x, gamma, beta, y, mean, rstd);
   if (ln_grid_supported(s, dtype, false))
     return launch_ln_grid_fwd(L, s, dtype, x, gamma, beta, y, mean, rstd);
   const long long points = s.outer * s.inner;
@@ -234,22 +236,24 @@ cudaError_t launch_ln_bwd(const Launch &L, const NormShape &s, int dtype, const 
   const long long points = s.outer * s.inner;
   const float inv_c = 1.0f / (float)s.C;
   cudaError_t err;
-  int nparts = 0;
   const bool params = dgamma || dbeta;
-  if (ln_pipe_supported(s, dtype, true)) {
-    err = launch_ln_pipe_bwd(L, s, dtype, x, gamma, mean, rstd, dy, dx,
-                             params ? partial : nullptr, &nparts);
-    if (err != cudaSuccess || !params) return err;
-    return launch_reduce_rows(L, partial, nparts, 2LL * s.C, 0, s.C, 1, dgamma, dbeta);
-  }
-  if (ln_grid_supported(s, dtype, true)) {
-    err = launch_ln_grid_bwd(L, s, dtype, x, gamma, mean, rstd, dy, dx,
-                             params ? partial : nullptr, &nparts);
+  float *part = params ? partial : nullptr;
+  int nparts = 0;
+  bool done = true;
+  if (ln_pipe_supported(s, dtype, true))
+    err = launch_ln_pipe_bwd(L, s, dtype, x, gamma, mean, rstd, dy, dx, part, &nparts);
+  else if (ln_rows_supported(s, dtype, true))
+    err = launch_ln_rows_bwd(L, s, dtype, x, gamma, mean, rstd, dy, dx, part, &nparts);
+  else if (ln_grid_supported(s, dtype, true))
+    err = launch_ln_grid_bwd(L, s, dtype, x, gamma, mean, rstd, dy, dx, part, &nparts);
+  else
+    done = false;
+  if (done) {
     if (err != cudaSuccess || !params) return err;
     return launch_reduce_rows(L, partial, nparts, 2LL * s.C, 0, s.C, 1, dgamma, dbeta);
   }
   // the parameter gradients first: dx may overwrite dy
-  if (dgamma || dbeta) {
+  if (params) {
     int slices;
     launch_begin(L);
     if (s.inner == 1) {

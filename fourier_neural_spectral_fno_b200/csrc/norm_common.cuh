@@ -41,11 +41,38 @@ template <> struct Pack<float, 4> {
   __device__ __forceinline__ void zero() { r = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void get(float *f) const { f[0] = r.x; f[1] = r.y; f[2] = r.z; f[3] = r.w; }
   __device__ __forceinline__ void set(const float *f) { r = make_float4(f[0], f[1], f[2], f[3]); }
+  __device__ __forceinline__ void get2(f32x2 *p) const {
+    p[0] = f2pack(r.x, r.y);
+    p[1] = f2pack(r.z, r.w);
+  }
+  __device__ __forceinline__ void set2(const f32x2 *p) {
+    f2unpack(p[0], r.x, r.y);
+    f2unpack(p[1], r.z, r.w);
+  }
 };
 template <> struct Pack<__half, 8> {
   uint4 r;
   __device__ __forceinline__ void keep() {
     asm volatile("" : "+r"(r.x), "+r"(r.y), "+r"(r.z), "+r"(r.w));
+  }
+  __device__ __forceinline__ void get2(f32x2 *p) const {
+    const unsigned w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float a, b;
+      word_get<__half>(w[i], a, b);
+      p[i] = f2pack(a, b);
+    }
+  }
+  __device__ __forceinline__ void set2(const f32x2 *p) {
+    unsigned w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float a, b;
+      f2unpack(p[i], a, b);
+      w[i] = word_set<__half>(a, b);
+    }
+    r = make_uint4(w[0], w[1], w[2], w[3]);
   }
   __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void get(float *f) const {
@@ -71,6 +98,25 @@ template <> struct Pack<__nv_bfloat16, 8> {
   uint4 r;
   __device__ __forceinline__ void keep() {
     asm volatile("" : "+r"(r.x), "+r"(r.y), "+r"(r.z), "+r"(r.w));
+  }
+  __device__ __forceinline__ void get2(f32x2 *p) const {
+    const unsigned w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float a, b;
+      word_get<__nv_bfloat16>(w[i], a, b);
+      p[i] = f2pack(a, b);
+    }
+  }
+  __device__ __forceinline__ void set2(const f32x2 *p) {
+    unsigned w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float a, b;
+      f2unpack(p[i], a, b);
+      w[i] = word_set<__nv_bfloat16>(a, b);
+    }
+    r = make_uint4(w[0], w[1], w[2], w[3]);
   }
   __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
   // a bfloat16 is the upper half of the float32 of the same value
@@ -155,7 +201,15 @@ cudaError_t launch_ln_grid_bwd(const Launch &L, const NormShape &s, int dtype, c
                                const void *gamma, const float *mean, const float *rstd,
                                const void *dy, void *dx, float *partial, int *nparts);
 
-// the same as a TMA pipeline, at most 64 channels (norm_pipe.cu)
+// rows (inner == 1), values held in registers (norm_rows.cu); outputs as above
+bool ln_rows_supported(const NormShape &s, int dtype, bool bwd);
+cudaError_t launch_ln_rows_fwd(const Launch &L, const NormShape &s, int dtype, const void *x,
+                               const void *gamma, const void *beta, void *y, float *mean,
+                               float *rstd);
+cudaError_t launch_ln_rows_bwd(const Launch &L, const NormShape &s, int dtype, const void *x,
+                               const void *gamma, const float *mean, const float *rstd,
+                               const void *dy, void *dx, float *partial, int *nparts);
+// the grid layout as a TMA pipeline, at most 64 channels (norm_pipe.cu)
 bool ln_pipe_supported(const NormShape &s, int dtype, bool bwd);
 cudaError_t launch_ln_pipe_fwd(const Launch &L, const NormShape &s, int dtype, const void *x,
                                const void *gamma, const void *beta, void *y, float *mean,
