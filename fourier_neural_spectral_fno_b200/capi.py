@@ -479,18 +479,15 @@ def fno_adam_step_clipped(theta, m, v, grad, param_out, step: int, lr: float, no
     (float32 device tensor of two, from :func:`fno_grad_norm`).
     ``skip_nonfinite``: a norm that is not finite leaves the state as it is."""
     out_code = _dtype_code_of(param_out) if param_out is not None else FNO_F32
-    n, dev = theta.numel(), theta.device
+    n, dev, f32 = theta.numel(), _device_index(theta, "theta"), _torch_dtypes()[0]
     for t, name in ((theta, "theta"), (m, "m"), (v, "v"), (grad, "grad")):
-        _check_tensor(t, name, FNO_F32, n, dev)
+        _check_tensor(t, name, f32, n, dev)
     if param_out is not None:
-        _check_tensor(param_out, "param_out", out_code, n, dev)
-    _check_tensor(norm, "norm", FNO_F32, 2, dev)
-    with _On(dev, stream) as st:
-        _check(load().fno_adam_step_clipped(n, _ptr(theta), _ptr(m), _ptr(v), _ptr(grad),
-                                            _ptr(param_out), out_code, int(step), float(lr),
-                                            float(beta1), float(beta2), float(eps),
-                                            float(weight_decay), float(grad_scale), _ptr(norm),
-                                            1 if skip_nonfinite else 0, st))
+        _check_tensor(param_out, "param_out", param_out.dtype, n, dev)
+    _check_tensor(norm, "norm", f32, 2, dev)
+    _run(load().fno_adam_step_clipped, dev, stream, n, _ptr(theta), _ptr(m), _ptr(v), _ptr(grad),
+         _ptr(param_out), out_code, int(step), float(lr), float(beta1), float(beta2), float(eps),
+         float(weight_decay), float(grad_scale), _ptr(norm), 1 if skip_nonfinite else 0)
 
 
 # --------------------------------------------------------------------------
@@ -510,51 +507,58 @@ def _torch_dtypes():
 _TORCH_DTYPES = None
 
 
-def _check_tensor(t, name: str, code: int, numel: int, device=None) -> None:
-    if t.dtype != _torch_dtypes()[code]:
-        raise ValueError(f"{name} is {t.dtype}, expected {_torch_dtypes()[code]}")
+def _device_index(t, name: str) -> int:
+    """The CUDA device of a tensor; a tensor on the host is refused (the kernels
+    would read its address on the device)."""
+    i = t.get_device()
+    if i < 0:
+        raise ValueError(f"{name} is on {t.device}, expected a CUDA device")
+    return i
+
+
+def _check_tensor(t, name: str, dtype, numel: int, device: int) -> None:
+    if t.dtype is dtype and t.numel() == numel and t.get_device() == device and t.is_contiguous():
+        return
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
     if t.numel() != numel:
         raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} is not contiguous")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, expected device {device}")
+    raise ValueError(f"{name} is not contiguous")
 
 
-def _scratch(nbytes: int, device, ws, stream):
-    """The caller's workspace, or a fresh one that is not reused before the work
-    of the given stream is done with it."""
+def _scratch(nbytes: int, like, ws, stream):
+    """The caller's workspace, or a fresh one on the device of `like` that is not
+    reused before the work of the given stream is done with it."""
     import torch
     if ws is not None:
-        if ws.device != device:
-            raise ValueError(f"ws is on {ws.device}, expected {device}")
+        if ws.get_device() != like.get_device():
+            raise ValueError(f"ws is on {ws.device}, expected {like.device}")
         return ws, ws.numel() * ws.element_size()
-    ws, nb = _workspace(nbytes, device, None)
+    ws, nb = _workspace(nbytes, like.device, None)
     if stream is not None and ws.is_cuda:
         ws.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                         else torch.cuda.ExternalStream(stream, device=device))
+                         else torch.cuda.ExternalStream(stream, device=like.device))
     return ws, nb
 
 
-class _On:
-    """The tensors' device as the current one for a call, and the stream to use:
-    the given one, else that device's current stream."""
-
-    def __init__(self, device, stream):
-        import torch
-        self.guard = None
-        if device.type == "cuda" and device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(device)
-        self.stream = stream
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return _stream(self.stream)
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _run(fn, device: int, stream, *args) -> None:
+    """``fn(*args, stream)`` with the tensors' device as the current one, on the
+    given stream or that device's current one."""
+    import torch
+    c = torch._C
+    if stream is None:
+        stream = c._cuda_getCurrentRawStream(device)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if device < 0 or device == c._cuda_getDevice():
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, stream)
+    if rc != FNO_OK:
+        raise FnoError(rc, last_error())
 
 
 def layer_norm_desc(outer: int, channels: int, inner: int = 1, dtype: str = "f32",
@@ -574,32 +578,25 @@ def fno_layer_norm_workspace_size(desc: NormDesc) -> int:
     return n
 
 
-def _check_norm_tensors(desc: NormDesc, big, channel, stats, grads=()):
-    dev = big[0][0].device
-    points = desc.outer * desc.inner
-    for t, name in big:
-        _check_tensor(t, name, desc.dtype, points * desc.channels, dev)
-    for t, name in channel:
-        if t is not None:
-            _check_tensor(t, name, desc.dtype, desc.channels, dev)
-    for t, name in stats:
-        if t is not None:
-            _check_tensor(t, name, FNO_F32, points, dev)
-    for t, name in grads:
-        if t is not None:
-            _check_tensor(t, name, FNO_F32, desc.channels, dev)
-    return dev
-
-
 def fno_layer_norm_fwd(desc: NormDesc, x, gamma, beta, y, mean=None, rstd=None, stream=None):
     """y = (x - mean) rstd gamma + beta over the channels; ``y`` may be ``x``.
     ``gamma`` / ``beta`` None: 1 / 0.  ``mean``, ``rstd`` (float32, [outer][inner]):
     what the backward reads."""
-    dev = _check_norm_tensors(desc, ((x, "x"), (y, "y")), ((gamma, "gamma"), (beta, "beta")),
-                              ((mean, "mean"), (rstd, "rstd")))
-    with _On(dev, stream) as st:
-        _check(load().fno_layer_norm_fwd(ctypes.byref(desc), _ptr(x), _ptr(gamma), _ptr(beta),
-                                         _ptr(y), _ptr(mean), _ptr(rstd), st))
+    dev = _device_index(x, "x")
+    types = _torch_dtypes()
+    dt, c, points = types[desc.dtype], desc.channels, desc.outer * desc.inner
+    _check_tensor(x, "x", dt, points * c, dev)
+    _check_tensor(y, "y", dt, points * c, dev)
+    if gamma is not None:
+        _check_tensor(gamma, "gamma", dt, c, dev)
+    if beta is not None:
+        _check_tensor(beta, "beta", dt, c, dev)
+    if mean is not None:
+        _check_tensor(mean, "mean", types[0], points, dev)
+    if rstd is not None:
+        _check_tensor(rstd, "rstd", types[0], points, dev)
+    _run(load().fno_layer_norm_fwd, dev, stream, ctypes.byref(desc), x.data_ptr(), _ptr(gamma),
+         _ptr(beta), y.data_ptr(), _ptr(mean), _ptr(rstd))
     return y
 
 
@@ -607,17 +604,26 @@ def fno_layer_norm_bwd(desc: NormDesc, x, gamma, mean, rstd, dy, dx, dgamma=None
                        ws=None, stream=None):
     """Adjoint of :func:`fno_layer_norm_fwd`: dx (may be ``dy``) and, where given,
     dgamma and dbeta (float32)."""
-    dev = _check_norm_tensors(desc, ((x, "x"), (dy, "dy"), (dx, "dx")), ((gamma, "gamma"),),
-                              ((mean, "mean"), (rstd, "rstd")),
-                              ((dgamma, "dgamma"), (dbeta, "dbeta")))
-    with _On(dev, stream) as st:
-        nb = 0
-        if dgamma is not None or dbeta is not None:
-            ws, nb = _scratch(fno_layer_norm_workspace_size(desc) if ws is None else 0, dev, ws,
-                              stream)
-        _check(load().fno_layer_norm_bwd(ctypes.byref(desc), _ptr(x), _ptr(gamma), _ptr(mean),
-                                         _ptr(rstd), _ptr(dy), _ptr(dx), _ptr(dgamma),
-                                         _ptr(dbeta), _ptr(ws), nb, st))
+    dev = _device_index(x, "x")
+    types = _torch_dtypes()
+    dt, f32, c, points = types[desc.dtype], types[0], desc.channels, desc.outer * desc.inner
+    _check_tensor(x, "x", dt, points * c, dev)
+    _check_tensor(dy, "dy", dt, points * c, dev)
+    _check_tensor(dx, "dx", dt, points * c, dev)
+    if gamma is not None:
+        _check_tensor(gamma, "gamma", dt, c, dev)
+    _check_tensor(mean, "mean", f32, points, dev)
+    _check_tensor(rstd, "rstd", f32, points, dev)
+    nb = 0
+    if dgamma is not None:
+        _check_tensor(dgamma, "dgamma", f32, c, dev)
+    if dbeta is not None:
+        _check_tensor(dbeta, "dbeta", f32, c, dev)
+    if dgamma is not None or dbeta is not None:
+        ws, nb = _scratch(fno_layer_norm_workspace_size(desc) if ws is None else 0, x, ws, stream)
+    _run(load().fno_layer_norm_bwd, dev, stream, ctypes.byref(desc), x.data_ptr(), _ptr(gamma),
+         mean.data_ptr(), rstd.data_ptr(), dy.data_ptr(), dx.data_ptr(), _ptr(dgamma),
+         _ptr(dbeta), _ptr(ws), nb)
     return dx, dgamma, dbeta
 
 
@@ -631,13 +637,14 @@ class GradList:
         if not grads:
             raise ValueError("no gradients given")
         self.dtype = _dtype_code_of(grads[0])
-        self.device = grads[0].device
+        self.device = _device_index(grads[0], "grads[0]")
         targets = grads if out is None else list(out)
         if len(targets) != len(grads):
             raise ValueError(f"{len(targets)} outputs for {len(grads)} gradients")
+        dt = grads[0].dtype
         for k, (g, o) in enumerate(zip(grads, targets)):
-            _check_tensor(g, f"grads[{k}]", self.dtype, g.numel(), self.device)
-            _check_tensor(o, f"out[{k}]", self.dtype, g.numel(), self.device)
+            _check_tensor(g, f"grads[{k}]", dt, g.numel(), self.device)
+            _check_tensor(o, f"out[{k}]", dt, g.numel(), self.device)
         n = len(grads)
         self.n = n
         self.tensors = (grads, targets)     # keeps the memory alive
@@ -692,12 +699,10 @@ def fno_grad_norm(grads, max_norm: float, norm, grad_scale: float = 1.0, ws=None
     ``grad_scale`` times the gradients and the factor min(1, max_norm / norm).
     ``grads``: a :class:`GradList` or a sequence of tensors."""
     gl = _as_grad_list(grads)
-    _check_tensor(norm, "norm", FNO_F32, 2, gl.device)
-    with _On(gl.device, stream) as st:
-        ws, nb = _scratch(fno_grad_norm_workspace_size(gl) if ws is None else 0, gl.device, ws,
-                          stream)
-        _check(load().fno_grad_norm(gl.n, gl.grads, gl.sizes, gl.dtype, float(grad_scale),
-                                    float(max_norm), _ptr(norm), _ptr(ws), nb, st))
+    _check_tensor(norm, "norm", _torch_dtypes()[0], 2, gl.device)
+    ws, nb = _scratch(fno_grad_norm_workspace_size(gl) if ws is None else 0, norm, ws, stream)
+    _run(load().fno_grad_norm, gl.device, stream, gl.n, gl.grads, gl.sizes, gl.dtype, grad_scale,
+         max_norm, norm.data_ptr(), ws.data_ptr(), nb)
     return norm
 
 
@@ -705,11 +710,8 @@ def fno_clip_grads(grads, max_norm: float, norm, grad_scale: float = 1.0, ws=Non
     """:func:`fno_grad_norm`, then every gradient times ``grad_scale * norm[1]``,
     in place or into the list's ``out`` tensors."""
     gl = _as_grad_list(grads)
-    _check_tensor(norm, "norm", FNO_F32, 2, gl.device)
-    with _On(gl.device, stream) as st:
-        ws, nb = _scratch(fno_grad_norm_workspace_size(gl) if ws is None else 0, gl.device, ws,
-                          stream)
-        _check(load().fno_clip_grads(gl.n, gl.grads, gl.out, gl.sizes, gl.dtype,
-                                     float(grad_scale), float(max_norm), _ptr(norm), _ptr(ws), nb,
-                                     st))
+    _check_tensor(norm, "norm", _torch_dtypes()[0], 2, gl.device)
+    ws, nb = _scratch(fno_grad_norm_workspace_size(gl) if ws is None else 0, norm, ws, stream)
+    _run(load().fno_clip_grads, gl.device, stream, gl.n, gl.grads, gl.out, gl.sizes, gl.dtype,
+         grad_scale, max_norm, norm.data_ptr(), ws.data_ptr(), nb)
     return norm

@@ -11,8 +11,18 @@
 //
 // The tensors' pointers and sizes travel in the launch's parameters (nothing to
 // upload, and a captured graph holds them).  The tensors are cut into chunks of
-// kChunkBytes; a CTA takes every gridDim-th chunk and finds its tensor by
-// bisection over the running chunk counts.
+// 4 KB, one for a warp at a time (many short parameters then still spread over
+// the GPU); a warp finds its chunk's tensor by bisection over the running chunk
+// counts, once per tensor.
+//
+// Few bytes: one launch of one thread-block cluster, whose CTAs read each other's
+// sums through distributed shared memory (norm, factor and scaling in it).  Else
+// one launch for the sums, which runs from the last chunk to the first so that
+// the next reader of the gradients, from the first on, finds them in L2, and one
+// that adds up the sums and scales (or only writes the norm); the second is
+// launched while the first runs (programmatic dependent launch).
+// Measured (us): see the launchers.
+#include <cooperative_groups.h>
 #include <math.h>
 
 #include "fno_common.cuh"
@@ -23,26 +33,42 @@ namespace fno {
 namespace {
 
 constexpr int CT = 256;                      // threads per CTA
-constexpr int kVecs = 8;                     // 16-byte groups per thread and chunk
-constexpr int kChunkBytes = CT * kVecs * 16;
+constexpr int kVecs = 8;                     // 16-byte groups per lane and chunk
+constexpr int kChunkBytes = 32 * kVecs * 16;
+constexpr int ST = 1024;                     // threads per CTA of the cluster form
+constexpr int kCluster = 8;
 
-struct TensorTable {
-  const void *in[kClipTensors];
-  void *out[kClipTensors];
-  long long n[kClipTensors];
-  int first[kClipTensors + 1];               // chunks before each tensor
+template <int N> struct TensorTable {
+  const void *in[N];
+  void *out[N];
+  long long n[N];
+  int first[N + 1];                          // chunks before each tensor
   int count;
 };
 
-// tensor of a chunk: the last one with first[t] <= chunk (empty ones excluded)
-__device__ __forceinline__ int find_tensor(const TensorTable &tab, int chunk) {
-  int lo = 0, hi = tab.count - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (tab.first[mid] <= chunk) lo = mid;
-    else hi = mid - 1;
+// A warp's place in the table: the tensor of its last chunk.
+struct Place {
+  int t = 0, lo = 0, hi = 0;                 // tensor t has the chunks lo .. hi - 1
+};
+
+// a chunk's tensor, first element and elements
+template <int N>
+__device__ __forceinline__ void find(const TensorTable<N> &tab, int chunk, int elems, Place &p,
+                                     long long &off, int &n) {
+  if (chunk < p.lo || chunk >= p.hi) {
+    int lo = 0, hi = tab.count - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (tab.first[mid] <= chunk) lo = mid;
+      else hi = mid - 1;
+    }
+    p.t = lo;
+    p.lo = tab.first[lo];
+    p.hi = tab.first[lo + 1];
   }
-  return lo;
+  off = (long long)(chunk - p.lo) * elems;
+  const long long left = tab.n[p.t] - off;
+  n = (int)(left < elems ? left : elems);
 }
 
 template <typename T> struct Vec16 {
@@ -76,135 +102,192 @@ __device__ __forceinline__ double warp_sum(double v) {
   return v;
 }
 
-// the CTA's sum, in thread 0
-__device__ __forceinline__ double cta_sum(double v, double *sh) {
+// the CTA's sum, in every thread
+template <int THREADS> __device__ __forceinline__ double cta_sum(double v, double *sh) {
   v = warp_sum(v);
   if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
   __syncthreads();
   double t = 0.0;
-  if (threadIdx.x == 0)
-    for (int i = 0; i < CT / 32; ++i) t += sh[i];
+#pragma unroll
+  for (int i = 0; i < THREADS / 32; ++i) t += sh[i];
   return t;
 }
 
-// partial[blockIdx] = sum of the squares of the CTA's chunks
-template <typename T>
-__global__ void __launch_bounds__(CT)
-    k_grad_sumsq(const __grid_constant__ TensorTable tab, double *__restrict__ partial) {
-  __shared__ double sh[CT / 32];
+// the lane's share of a chunk's squares
+template <typename T, int N>
+__device__ __forceinline__ double chunk_sq(const TensorTable<N> &tab, int chunk, Place &p) {
   constexpr int VN = Vec16<T>::N;
-  constexpr long long CE = kChunkBytes / sizeof(T);
-  const int chunks = tab.first[tab.count];
+  const int lane = threadIdx.x & 31;
+  long long off;
+  int n, done = 0;
+  find(tab, chunk, kChunkBytes / (int)sizeof(T), p, off, n);
+  const T *src = static_cast<const T *>(tab.in[p.t]) + off;
   double acc = 0.0;
-  for (int ch = blockIdx.x; ch < chunks; ch += gridDim.x) {
-    const int t = find_tensor(tab, ch);
-    const long long off = (ch - tab.first[t]) * CE;
-    const long long left = tab.n[t] - off;
-    const int n = (int)(left < CE ? left : CE);
-    const T *src = static_cast<const T *>(tab.in[t]) + off;
-    int done = 0;
-    if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
-      const uint4 *v = reinterpret_cast<const uint4 *>(src);
-      const int nv = n / VN;
-      done = nv * VN;
-      Vec16<T> g[kVecs];
+  if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
+    const uint4 *v = reinterpret_cast<const uint4 *>(src);
+    const int nv = n / VN;
+    done = nv * VN;
+    Vec16<T> g[kVecs];
 #pragma unroll
-      for (int j = 0; j < kVecs; ++j) {
-        const int i = threadIdx.x + j * CT;
-        g[j].raw = i < nv ? __ldg(v + i) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int j = 0; j < kVecs; ++j)
-        if (threadIdx.x + j * CT < nv) acc += sq_group<T>(g[j]);
+    for (int j = 0; j < kVecs; ++j) {
+      const int i = lane + j * 32;
+      g[j].raw = i < nv ? v[i] : make_uint4(0, 0, 0, 0);
     }
-    for (int i = done + threadIdx.x; i < n; i += CT) {
-      const double g = (double)to_f<T>(src[i]);
-      acc = fma(g, g, acc);
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j)
+      if (lane + j * 32 < nv) acc += sq_group<T>(g[j]);
+  }
+  for (int i = done + lane; i < n; i += 32) {
+    const double g = (double)to_f<T>(src[i]);
+    acc = fma(g, g, acc);
+  }
+  return acc;
+}
+
+// out = g f over a chunk; in place and with f == 1 nothing changes and nothing is
+// written
+template <typename T, int N>
+__device__ __forceinline__ void chunk_scale(const TensorTable<N> &tab, int chunk, Place &p,
+                                            float f) {
+  constexpr int VN = Vec16<T>::N;
+  const int lane = threadIdx.x & 31;
+  long long off;
+  int n, done = 0;
+  find(tab, chunk, kChunkBytes / (int)sizeof(T), p, off, n);
+  if (f == 1.f && tab.in[p.t] == tab.out[p.t]) return;
+  const T *src = static_cast<const T *>(tab.in[p.t]) + off;
+  T *dst = static_cast<T *>(tab.out[p.t]) + off;
+  if (((reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst)) & 15) == 0) {
+    const int nv = n / VN;
+    done = nv * VN;
+    Vec16<T> g[kVecs];
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      const int i = lane + j * 32;
+      if (i < nv) g[j].raw = reinterpret_cast<const uint4 *>(src)[i];
+    }
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      const int i = lane + j * 32;
+      if (i < nv) {
+#pragma unroll
+        for (int k = 0; k < VN; ++k) g[j].set(k, g[j].get(k) * f);
+        reinterpret_cast<uint4 *>(dst)[i] = g[j].raw;
+      }
     }
   }
-  acc = cta_sum(acc, sh);
+  for (int i = done + lane; i < n; i += 32) dst[i] = from_f<T>(to_f<T>(src[i]) * f);
+}
+
+// norm[0] = the norm, norm[1] = the factor, of a sum of squares
+__device__ __forceinline__ float2 norm_of(double sum, double scale, double max_norm) {
+  const double nm = sqrt(sum) * scale;
+  return make_float2((float)nm, nm <= max_norm ? 1.f : (float)(max_norm / nm));
+}
+
+// partial[blockIdx] = sum of the squares of the CTA's chunks
+template <typename T, int N>
+__global__ void __launch_bounds__(CT)
+    k_grad_sumsq(const __grid_constant__ TensorTable<N> tab, double *__restrict__ partial) {
+  __shared__ double sh[CT / 32];
+  cudaTriggerProgrammaticLaunchCompletion();   // the next launch may be set up meanwhile
+  const int chunks = tab.first[tab.count], step = gridDim.x * (CT / 32);
+  double acc = 0.0;
+  Place p;
+  for (int ch = chunks - 1 - (int)(blockIdx.x * (CT / 32) + (threadIdx.x >> 5)); ch >= 0; ch -= step)
+    acc += chunk_sq<T>(tab, ch, p);
+  acc = cta_sum<CT>(acc, sh);
   if (threadIdx.x == 0) partial[blockIdx.x] = acc;
 }
 
-// norm[0] = the norm, norm[1] = the factor
-__global__ void __launch_bounds__(CT)
-    k_grad_norm(const double *__restrict__ partial, int nparts, double scale, double max_norm,
-                float *__restrict__ norm) {
-  __shared__ double sh[CT / 32];
+// the sum of all partial sums, in every thread; `partial` comes from the launch
+// before
+__device__ __forceinline__ double all_parts(const double *partial, int nparts, double *sh) {
+  cudaGridDependencySynchronize();
   double acc = 0.0;
-  for (int i = threadIdx.x; i < nparts; i += CT) acc += partial[i];
-  acc = cta_sum(acc, sh);
-  if (threadIdx.x == 0) {
-    const double nm = sqrt(acc) * scale;
-    norm[0] = (float)nm;
-    norm[1] = nm <= max_norm ? 1.f : (float)(max_norm / nm);
-  }
+  for (int i = threadIdx.x; i < nparts; i += CT) acc += __ldcg(partial + i);
+  return cta_sum<CT>(acc, sh);
 }
 
-// out = g (scale factor); in place and with a multiplier of one nothing changes
-// and nothing is written
-template <typename T>
 __global__ void __launch_bounds__(CT)
-    k_grad_scale(const __grid_constant__ TensorTable tab, const float *__restrict__ norm,
-                 float scale) {
-  constexpr int VN = Vec16<T>::N;
-  constexpr long long CE = kChunkBytes / sizeof(T);
-  const int chunks = tab.first[tab.count];
-  const float f = norm[1] * scale;
-  for (int ch = blockIdx.x; ch < chunks; ch += gridDim.x) {
-    const int t = find_tensor(tab, ch);
-    if (f == 1.f && tab.in[t] == tab.out[t]) continue;
-    const long long off = (ch - tab.first[t]) * CE;
-    const long long left = tab.n[t] - off;
-    const int n = (int)(left < CE ? left : CE);
-    const T *src = static_cast<const T *>(tab.in[t]) + off;
-    T *dst = static_cast<T *>(tab.out[t]) + off;
-    int done = 0;
-    if (((reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst)) & 15) == 0) {
-      const int nv = n / VN;
-      done = nv * VN;
-      Vec16<T> g[kVecs];
-#pragma unroll
-      for (int j = 0; j < kVecs; ++j) {
-        const int i = threadIdx.x + j * CT;
-        if (i < nv) g[j].raw = reinterpret_cast<const uint4 *>(src)[i];
-      }
-#pragma unroll
-      for (int j = 0; j < kVecs; ++j) {
-        const int i = threadIdx.x + j * CT;
-        if (i < nv) {
-#pragma unroll
-          for (int k = 0; k < VN; ++k) g[j].set(k, g[j].get(k) * f);
-          reinterpret_cast<uint4 *>(dst)[i] = g[j].raw;
-        }
-      }
-    }
-    for (int i = done + threadIdx.x; i < n; i += CT) dst[i] = from_f<T>(to_f<T>(src[i]) * f);
+    k_grad_norm(const double *partial, int nparts, double scale, double max_norm, float *norm) {
+  __shared__ double sh[CT / 32];
+  const float2 r = norm_of(all_parts(partial, nparts, sh), scale, max_norm);
+  if (threadIdx.x == 0) {
+    norm[0] = r.x;
+    norm[1] = r.y;
   }
 }
 
-// Fill `tab` from tensor `at` on; returns the tensors taken (empty ones are
-// passed over, so it may take more than it lists), and false where the chunks
-// do not fit an int.
-int fill(TensorTable &tab, int at, int n, const void *const *in, void *const *out,
+// every CTA adds up the partial sums for itself; CTA 0 writes the norm
+template <typename T, int N>
+__global__ void __launch_bounds__(CT)
+    k_grad_scale(const __grid_constant__ TensorTable<N> tab, const double *partial, int nparts,
+                 double scale, double max_norm, float grad_scale, float *norm) {
+  __shared__ double sh[CT / 32];
+  const float2 r = norm_of(all_parts(partial, nparts, sh), scale, max_norm);
+  if (norm && blockIdx.x == 0 && threadIdx.x == 0) {
+    norm[0] = r.x;
+    norm[1] = r.y;
+  }
+  const float f = r.y * grad_scale;
+  const int chunks = tab.first[tab.count], step = gridDim.x * (CT / 32);
+  Place p;
+  for (int ch = blockIdx.x * (CT / 32) + (threadIdx.x >> 5); ch < chunks; ch += step)
+    chunk_scale<T>(tab, ch, p, f);
+}
+
+// all of it by one cluster
+template <typename T, int N, bool SCALE>
+__global__ void __launch_bounds__(ST)
+    k_grad_cluster(const __grid_constant__ TensorTable<N> tab, double scale, double max_norm,
+                   float grad_scale, float *norm) {
+  __shared__ double sh[ST / 32];
+  __shared__ double mine;
+  namespace cg = cooperative_groups;
+  cg::cluster_group cl = cg::this_cluster();
+  const int chunks = tab.first[tab.count], step = gridDim.x * (ST / 32);
+  const int ch0 = blockIdx.x * (ST / 32) + (threadIdx.x >> 5);
+  double acc = 0.0;
+  Place p;
+  for (int ch = ch0; ch < chunks; ch += step) acc += chunk_sq<T>(tab, ch, p);
+  acc = cta_sum<ST>(acc, sh);
+  if (threadIdx.x == 0) mine = acc;
+  cl.sync();
+  double sum = 0.0;
+  for (int k = 0; k < (int)gridDim.x; ++k) sum += *cl.map_shared_rank(&mine, k);
+  cl.sync();   // no CTA leaves while another reads its sum
+  const float2 r = norm_of(sum, scale, max_norm);
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    norm[0] = r.x;
+    norm[1] = r.y;
+  }
+  if (SCALE) {
+    const float f = r.y * grad_scale;
+    for (int ch = ch0; ch < chunks; ch += step) chunk_scale<T>(tab, ch, p, f);
+  }
+}
+
+// Fill `tab` from tensor `at` on, passing over empty ones; returns the tensor
+// after the last one taken.
+template <int N>
+int fill(TensorTable<N> &tab, int at, int n, const void *const *in, void *const *out,
          const int64_t *sizes, int elem) {
   const long long ce = kChunkBytes / elem;
-  long long chunks = 0;
+  int chunks = 0;   // at most 2^40 elements in all: below 2^30 chunks and one a tensor
   tab.count = 0;
   int i = at;
-  for (; i < n && tab.count < kClipTensors; ++i) {
+  for (; i < n && tab.count < N; ++i) {
     if (sizes[i] == 0) continue;
-    const long long c = (sizes[i] + ce - 1) / ce;
-    if (chunks + c > 0x7fffffffLL - kNormCTAs) break;
     tab.in[tab.count] = in[i];
     tab.out[tab.count] = out ? out[i] : const_cast<void *>(in[i]);
     tab.n[tab.count] = sizes[i];
-    tab.first[tab.count] = (int)chunks;
-    chunks += c;
+    tab.first[tab.count] = chunks;
+    chunks += (int)((sizes[i] + ce - 1) / ce);
     ++tab.count;
   }
-  tab.first[tab.count] = (int)chunks;
-  return i - at;
+  tab.first[tab.count] = chunks;
+  return i;
 }
 
 #define FNO_DISPATCH_T(dtype, ...)                                \
@@ -222,52 +305,115 @@ int fill(TensorTable &tab, int at, int n, const void *const *in, void *const *ou
   } while (0)
 
 int clip_grid(const Launch &L, int chunks) {
-  long long cap = 4LL * L.num_sms;
+  const int ctas = (chunks + CT / 32 - 1) / (CT / 32);
+  int cap = 4 * L.num_sms;
   if (cap > kNormCTAs) cap = kNormCTAs;
-  return (int)(chunks < cap ? chunks : cap);
+  return ctas < cap ? ctas : cap;
 }
 
-}  // namespace
+cudaLaunchConfig_t config(const Launch &L, int grid, int threads, cudaLaunchAttribute *attr) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(grid);
+  c.blockDim = dim3(threads);
+  c.stream = L.stream;
+  c.attrs = attr;
+  c.numAttrs = 1;
+  return c;
+}
 
-cudaError_t launch_grad_norm(const Launch &L, int n, const void *const *grads,
-                             const int64_t *sizes, int dtype, float grad_scale, float max_norm,
-                             float *norm, double *partial) {
-  TensorTable tab;
+// a launch that may begin while the one before it still runs
+template <typename... P, typename... A>
+cudaError_t launch_dependent(const Launch &L, int grid, void (*kern)(P...), A... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  const cudaLaunchConfig_t c = config(L, grid, CT, &attr);
+  return cudaLaunchKernelEx(&c, kern, P(args)...);
+}
+
+template <typename T, int N>
+cudaError_t cluster(const Launch &L, const TensorTable<N> &tab, bool scale_too, double scale,
+                    double max_norm, float grad_scale, float *norm) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  const int ctas = (tab.first[tab.count] + ST / 32 - 1) / (ST / 32);
+  int grid = 1;
+  while (grid < ctas && grid < kCluster) grid *= 2;
+  attr.val.clusterDim.x = grid;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  const cudaLaunchConfig_t c = config(L, grid, ST, &attr);
+  if (scale_too)
+    return cudaLaunchKernelEx(&c, k_grad_cluster<T, N, true>, tab, scale, max_norm, grad_scale,
+                              norm);
+  return cudaLaunchKernelEx(&c, k_grad_cluster<T, N, false>, tab, scale, max_norm, grad_scale,
+                            norm);
+}
+
+// out == nullptr: the norm alone
+template <typename T, int N>
+cudaError_t run(const Launch &L, int n, const void *const *grads, void *const *out, bool scale_too,
+                const int64_t *sizes, float grad_scale, float max_norm, float *norm,
+                double *partial) {
+  const double scale = fabs((double)grad_scale), limit = (double)max_norm;
+  TensorTable<N> tab;
+  int at = fill(tab, 0, n, grads, out, sizes, sizeof(T));
+  if (at == n && tab.first[tab.count] <= kClusterChunks) {
+    launch_begin(L);
+    const cudaError_t err = cluster<T, N>(L, tab, scale_too, scale, limit, grad_scale, norm);
+    launch_end(L, scale_too ? "grad_clip" : "grad_norm");
+    return err;
+  }
   int nparts = 0;
-  for (int at = 0; at < n;) {
-    at += fill(tab, at, n, grads, nullptr, sizes, dtype == DT_F32 ? 4 : 2);
+  for (int from = 0; from < n;) {
+    if (from > 0 || at == 0) at = fill(tab, from, n, grads, out, sizes, sizeof(T));
+    from = at;
     if (tab.count == 0) continue;
     const int grid = clip_grid(L, tab.first[tab.count]);
     launch_begin(L);
-    FNO_DISPATCH_T(dtype, k_grad_sumsq<T><<<grid, CT, 0, L.stream>>>(tab, partial + nparts));
+    k_grad_sumsq<T, N><<<grid, CT, 0, L.stream>>>(tab, partial + nparts);
     const cudaError_t err = cudaGetLastError();
     launch_end(L, "grad_sumsq");
     if (err != cudaSuccess) return err;
     nparts += grid;
   }
-  launch_begin(L);
-  k_grad_norm<<<1, CT, 0, L.stream>>>(partial, nparts, fabs((double)grad_scale),
-                                      (double)max_norm, norm);
-  const cudaError_t err = cudaGetLastError();
-  launch_end(L, "grad_norm");
-  return err;
-}
-
-cudaError_t launch_grad_scale(const Launch &L, int n, const void *const *grads, void *const *out,
-                              const int64_t *sizes, int dtype, float grad_scale,
-                              const float *norm) {
-  TensorTable tab;
-  for (int at = 0; at < n;) {
-    at += fill(tab, at, n, grads, out, sizes, dtype == DT_F32 ? 4 : 2);
-    if (tab.count == 0) continue;
-    const int grid = clip_grid(L, tab.first[tab.count]);
+  if (!scale_too) {
     launch_begin(L);
-    FNO_DISPATCH_T(dtype, k_grad_scale<T><<<grid, CT, 0, L.stream>>>(tab, norm, grad_scale));
-    const cudaError_t err = cudaGetLastError();
+    const cudaError_t err =
+        launch_dependent(L, 1, k_grad_norm, (const double *)partial, nparts, scale, limit, norm);
+    launch_end(L, "grad_norm");
+    return err;
+  }
+  bool first = true;
+  for (int from = 0; from < n;) {
+    // a single table is still filled
+    if (n > N || !first) from = fill(tab, from, n, grads, out, sizes, sizeof(T));
+    else from = n;
+    if (tab.count == 0) continue;
+    launch_begin(L);
+    const int grid = clip_grid(L, tab.first[tab.count]);
+    const cudaError_t err =
+        launch_dependent(L, grid, k_grad_scale<T, N>, tab, (const double *)partial, nparts, scale,
+                         limit, grad_scale, first ? norm : nullptr);
     launch_end(L, "grad_scale");
     if (err != cudaSuccess) return err;
+    first = false;
   }
   return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_grad_norm(const Launch &L, int n, const void *const *grads, void *const *out,
+                             bool scale_too, const int64_t *sizes, int dtype, float grad_scale,
+                             float max_norm, float *norm, double *partial) {
+  cudaError_t err;
+  if (n <= kFewTensors)
+    FNO_DISPATCH_T(dtype, err = run<T, kFewTensors>(L, n, grads, out, scale_too, sizes, grad_scale,
+                                                    max_norm, norm, partial));
+  else
+    FNO_DISPATCH_T(dtype, err = run<T, kClipTensors>(L, n, grads, out, scale_too, sizes,
+                                                     grad_scale, max_norm, norm, partial));
+  return err;
 }
 
 }  // namespace fno

@@ -1231,8 +1231,8 @@ int fno_grad_norm(int n_tensors, const void *const *grads, const int64_t *sizes,
                        ws_bytes);
   if (rc) return rc;
   Launch L = make_launch(stream);
-  FNO_TRY(launch_grad_norm(L, n_tensors, grads, sizes, dtype, grad_scale, max_norm, norm,
-                           reinterpret_cast<double *>(ws)),
+  FNO_TRY(launch_grad_norm(L, n_tensors, grads, nullptr, false, sizes, dtype, grad_scale,
+                           max_norm, norm, reinterpret_cast<double *>(ws)),
           "gradient norm");
   g_err[0] = 0;
   return FNO_OK;
@@ -1246,10 +1246,8 @@ int fno_clip_grads(int n_tensors, const void *const *grads, void *const *out,
                        ws_bytes);
   if (rc) return rc;
   Launch L = make_launch(stream);
-  FNO_TRY(launch_grad_norm(L, n_tensors, grads, sizes, dtype, grad_scale, max_norm, norm,
-                           reinterpret_cast<double *>(ws)),
-          "gradient norm");
-  FNO_TRY(launch_grad_scale(L, n_tensors, grads, out, sizes, dtype, grad_scale, norm),
+  FNO_TRY(launch_grad_norm(L, n_tensors, grads, out, true, sizes, dtype, grad_scale, max_norm,
+                           norm, reinterpret_cast<double *>(ws)),
           "gradient clipping");
   g_err[0] = 0;
   return FNO_OK;

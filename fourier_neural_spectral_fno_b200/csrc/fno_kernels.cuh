@@ -288,16 +288,15 @@ cudaError_t launch_ln_bwd(const Launch &L, const NormShape &s, int dtype, const 
                           void *dx, float *dgamma, float *dbeta, float *partial);
 
 // ---- gradient norm and clipping (clip.cu) ----------------------------------
-constexpr int kClipTensors = 128;   // tensors of one launch (a 4 KB parameter block)
-constexpr int kNormCTAs = 1184;     // most partial sums of one launch
-// norm (device): [0] = |grad_scale| ||g||, [1] = min(1, max_norm / norm);
-// partial: kNormCTAs float64 for each kClipTensors tensors
-cudaError_t launch_grad_norm(const Launch &L, int n, const void *const *grads,
-                             const int64_t *sizes, int dtype, float grad_scale, float max_norm,
-                             float *norm, double *partial);
-// out[i] = grads[i] grad_scale norm[1]
-cudaError_t launch_grad_scale(const Launch &L, int n, const void *const *grads, void *const *out,
-                              const int64_t *sizes, int dtype, float grad_scale,
-                              const float *norm);
+constexpr int kFewTensors = 64;      // tensors of one launch: a 2 KB parameter block,
+constexpr int kClipTensors = 1024;   // or one of 29 KB
+constexpr int kNormCTAs = 1184;      // most partial sums of one launch
+constexpr int kClusterChunks = 1024; // most 4 KB chunks for the one-cluster form
+// norm (device): [0] = |grad_scale| ||g||, [1] = min(1, max_norm / norm); with
+// scale_too also out[i] = grads[i] grad_scale norm[1].  partial: kNormCTAs float64
+// for each kClipTensors tensors
+cudaError_t launch_grad_norm(const Launch &L, int n, const void *const *grads, void *const *out,
+                             bool scale_too, const int64_t *sizes, int dtype, float grad_scale,
+                             float max_norm, float *norm, double *partial);
 
 }  // namespace fno

@@ -409,7 +409,11 @@ LISTS = {
     "one": [1], "empty": [0], "empties": [0, 0, 5, 0], "pair": [7, 4099],
     "chunks": [8192, 8191, 8193, 16384, 16385, 3], "large": [3_000_001, 12, 1_500_000],
     "many": [1 + (i * 37) % 977 for i in range(700)],
-    "limit": [5] * 128, "limit+1": [5] * 129, "limit+0": [5] * 128 + [0] * 3,
+    # around the numbers of tensors and of 4 KB chunks that one launch takes
+    "few": [5] * 64, "few+1": [5] * 65, "few+0": [5] * 64 + [0] * 3,
+    "one-cluster": [1 << 20], "one-cluster+1": [1 << 20, 1],
+    "table": [1100] * 1024, "table+1": [1100] * 1025, "table+0": [1100] * 1024 + [0, 0],
+    "tables": [3 + (i * 91) % 5000 for i in range(2300)],
 }
 
 

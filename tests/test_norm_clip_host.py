@@ -143,7 +143,7 @@ def test_grad_norm_refuses(lib):
     n, g, s = _grad_args()
     need = capi.fno_grad_norm_workspace_size(n)
     assert lib.fno_grad_norm_workspace_size(0) == 0 and "n_tensors 0" in capi.last_error()
-    assert capi.fno_grad_norm_workspace_size(1000) > need
+    assert capi.fno_grad_norm_workspace_size(2000) > need
 
     def call(n=n, g=g, s=s, dtype=0, scale=1.0, mx=1.0, norm=256, ws=256, nb=need):
         rc = lib.fno_grad_norm(n, g, s, dtype, scale, mx, norm, ws, nb, None)
@@ -191,7 +191,27 @@ def test_adam_step_clipped_refuses(lib):
 
 # ------------------------------------------------------------- the binding
 
-def test_binding_refuses_layer_norm_tensors(lib):
+@pytest.fixture
+def host_tensors(monkeypatch):
+    """Let host tensors pass the binding's device check, for calls that the library
+    refuses before anything touches a device."""
+    monkeypatch.setattr(capi, "_device_index", lambda t, name: t.get_device())
+
+
+def test_binding_refuses_host_tensors(lib):
+    d = capi.layer_norm_desc(2, 8, 16)
+    x, c, s = torch.zeros(2, 8, 16), torch.zeros(8), torch.zeros(2, 16)
+    with pytest.raises(ValueError, match="x is on cpu"):
+        capi.fno_layer_norm_fwd(d, x, c, c, x)
+    with pytest.raises(ValueError, match="x is on cpu"):
+        capi.fno_layer_norm_bwd(d, x, c, s, s, x, x.clone())
+    with pytest.raises(ValueError, match="grads.0. is on cpu"):
+        capi.fno_clip_grads([x], 1.0, torch.zeros(2))
+    with pytest.raises(ValueError, match="theta is on cpu"):
+        capi.fno_adam_step_clipped(c, c, c, c, None, 1, 1e-3, torch.zeros(2))
+
+
+def test_binding_refuses_layer_norm_tensors(lib, host_tensors):
     d = capi.layer_norm_desc(2, 8, 16)
     x = torch.zeros(2, 8, 16)
     c, s = torch.zeros(8), torch.zeros(2, 16)
@@ -214,7 +234,7 @@ def test_binding_refuses_layer_norm_tensors(lib):
 @pytest.mark.parametrize("fn,arg", [("fwd", a) for a in ("x", "gamma", "beta", "y", "mean", "rstd")]
                          + [("bwd", a) for a in ("x", "gamma", "mean", "rstd", "dy", "dx",
                                                  "dgamma", "dbeta")])
-def test_binding_passes_each_pointer_in_place(lib, fn, arg):
+def test_binding_passes_each_pointer_in_place(lib, host_tensors, fn, arg):
     d = capi.layer_norm_desc(2, 8, 16)
     n = {"gamma": 8, "beta": 8, "dgamma": 8, "dbeta": 8, "mean": 32, "rstd": 32}
 
@@ -228,7 +248,7 @@ def test_binding_passes_each_pointer_in_place(lib, fn, arg):
         getattr(capi, "fno_layer_norm_" + fn)(d, stream=0, **{k: buf(k) for k in names})
 
 
-def test_binding_refuses_gradient_lists(lib):
+def test_binding_refuses_gradient_lists(lib, host_tensors):
     g = [torch.zeros(5), torch.zeros(0), torch.zeros(3, 2)]
     assert capi.grad_list(g).n == 3
     flat = torch.zeros(16)
@@ -255,7 +275,7 @@ def test_binding_refuses_gradient_lists(lib):
         capi.fno_clip_grads(g, 1.0, torch.zeros(2), grad_scale=float("inf"), stream=0)
 
 
-def test_binding_refuses_clipped_adam_tensors(lib):
+def test_binding_refuses_clipped_adam_tensors(lib, host_tensors):
     t = [torch.zeros(8) for _ in range(4)]
     norm = torch.zeros(2)
     for k, word in enumerate(("theta", "m", "v", "grad")):
