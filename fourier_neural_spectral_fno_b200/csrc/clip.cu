@@ -15,14 +15,17 @@
 // the GPU); a warp finds its chunk's tensor by bisection over the running chunk
 // counts, once per tensor.
 //
-// Few bytes: one launch of one thread-block cluster, whose CTAs read each other's
-// sums through distributed shared memory (norm, factor and scaling in it).  Else
-// one launch for the sums, which runs from the last chunk to the first so that
-// the next reader of the gradients, from the first on, finds them in L2, and one
-// that adds up the sums and scales (or only writes the norm); the second is
-// launched while the first runs (programmatic dependent launch).
-// Measured (us): see the launchers.
-#include <cooperative_groups.h>
+// At most one chunk for each warp of a CTA: one launch of one CTA.  Else one
+// launch for the sums, which runs from the last chunk to the first so that the
+// next reader of the gradients, from the first on, finds them in L2, and one that
+// adds up the sums and scales (or only writes the norm); the second is launched
+// while the first runs (programmatic dependent launch).  A cluster of eight CTAs
+// for up to 4 MB in one launch measured slower (18 parameters of 0.9 M float32:
+// 9.1 us against 3.5; 320 short bfloat16 ones, clipped: 29 against 6.3).
+//
+// Bound by HBM for many bytes (25.5 us for 37.8 M float32, 92 % of the copy rate;
+// clipped they no longer fit L2 and are read twice: 73.6 us), by the two launches
+// for few.
 #include <math.h>
 
 #include "fno_common.cuh"
@@ -35,8 +38,7 @@ namespace {
 constexpr int CT = 256;                      // threads per CTA
 constexpr int kVecs = 8;                     // 16-byte groups per lane and chunk
 constexpr int kChunkBytes = 32 * kVecs * 16;
-constexpr int ST = 1024;                     // threads per CTA of the cluster form
-constexpr int kCluster = 8;
+constexpr int ST = 1024;                     // threads of the one-CTA form
 
 template <int N> struct TensorTable {
   const void *in[N];
@@ -237,35 +239,23 @@ __global__ void __launch_bounds__(CT)
     chunk_scale<T>(tab, ch, p, f);
 }
 
-// all of it by one cluster
+// all of it by one CTA
 template <typename T, int N, bool SCALE>
 __global__ void __launch_bounds__(ST)
-    k_grad_cluster(const __grid_constant__ TensorTable<N> tab, double scale, double max_norm,
-                   float grad_scale, float *norm) {
+    k_grad_one(const __grid_constant__ TensorTable<N> tab, double scale, double max_norm,
+               float grad_scale, float *norm) {
   __shared__ double sh[ST / 32];
-  __shared__ double mine;
-  namespace cg = cooperative_groups;
-  cg::cluster_group cl = cg::this_cluster();
-  const int chunks = tab.first[tab.count], step = gridDim.x * (ST / 32);
-  const int ch0 = blockIdx.x * (ST / 32) + (threadIdx.x >> 5);
-  double acc = 0.0;
+  const int chunk = threadIdx.x >> 5;
+  const bool in = chunk < tab.first[tab.count];
   Place p;
-  for (int ch = ch0; ch < chunks; ch += step) acc += chunk_sq<T>(tab, ch, p);
+  double acc = in ? chunk_sq<T>(tab, chunk, p) : 0.0;
   acc = cta_sum<ST>(acc, sh);
-  if (threadIdx.x == 0) mine = acc;
-  cl.sync();
-  double sum = 0.0;
-  for (int k = 0; k < (int)gridDim.x; ++k) sum += *cl.map_shared_rank(&mine, k);
-  cl.sync();   // no CTA leaves while another reads its sum
-  const float2 r = norm_of(sum, scale, max_norm);
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
+  const float2 r = norm_of(acc, scale, max_norm);
+  if (threadIdx.x == 0) {
     norm[0] = r.x;
     norm[1] = r.y;
   }
-  if (SCALE) {
-    const float f = r.y * grad_scale;
-    for (int ch = ch0; ch < chunks; ch += step) chunk_scale<T>(tab, ch, p, f);
-  }
+  if (SCALE && in) chunk_scale<T>(tab, chunk, p, r.y * grad_scale);
 }
 
 // Fill `tab` from tensor `at` on, passing over empty ones; returns the tensor
@@ -311,45 +301,22 @@ int clip_grid(const Launch &L, int chunks) {
   return ctas < cap ? ctas : cap;
 }
 
-cudaLaunchConfig_t config(const Launch &L, int grid, int threads, cudaLaunchAttribute *attr) {
-  cudaLaunchConfig_t c{};
-  c.gridDim = dim3(grid);
-  c.blockDim = dim3(threads);
-  c.stream = L.stream;
-  c.attrs = attr;
-  c.numAttrs = 1;
-  return c;
-}
-
 // a launch that may begin while the one before it still runs
 template <typename... P, typename... A>
-cudaError_t launch_dependent(const Launch &L, int grid, void (*kern)(P...), A... args) {
+cudaError_t launch_dependent(const Launch &L, int grid, void (*kern)(P...),
+                             const A &...args) {
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
-  const cudaLaunchConfig_t c = config(L, grid, CT, &attr);
-  return cudaLaunchKernelEx(&c, kern, P(args)...);
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(grid);
+  c.blockDim = dim3(CT);
+  c.stream = L.stream;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kern, args...);
 }
 
-template <typename T, int N>
-cudaError_t cluster(const Launch &L, const TensorTable<N> &tab, bool scale_too, double scale,
-                    double max_norm, float grad_scale, float *norm) {
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  const int ctas = (tab.first[tab.count] + ST / 32 - 1) / (ST / 32);
-  int grid = 1;
-  while (grid < ctas && grid < kCluster) grid *= 2;
-  attr.val.clusterDim.x = grid;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  const cudaLaunchConfig_t c = config(L, grid, ST, &attr);
-  if (scale_too)
-    return cudaLaunchKernelEx(&c, k_grad_cluster<T, N, true>, tab, scale, max_norm, grad_scale,
-                              norm);
-  return cudaLaunchKernelEx(&c, k_grad_cluster<T, N, false>, tab, scale, max_norm, grad_scale,
-                            norm);
-}
-
-// out == nullptr: the norm alone
 template <typename T, int N>
 cudaError_t run(const Launch &L, int n, const void *const *grads, void *const *out, bool scale_too,
                 const int64_t *sizes, float grad_scale, float max_norm, float *norm,
@@ -357,9 +324,13 @@ cudaError_t run(const Launch &L, int n, const void *const *grads, void *const *o
   const double scale = fabs((double)grad_scale), limit = (double)max_norm;
   TensorTable<N> tab;
   int at = fill(tab, 0, n, grads, out, sizes, sizeof(T));
-  if (at == n && tab.first[tab.count] <= kClusterChunks) {
+  if (at == n && tab.first[tab.count] <= ST / 32) {
     launch_begin(L);
-    const cudaError_t err = cluster<T, N>(L, tab, scale_too, scale, limit, grad_scale, norm);
+    if (scale_too)
+      k_grad_one<T, N, true><<<1, ST, 0, L.stream>>>(tab, scale, limit, grad_scale, norm);
+    else
+      k_grad_one<T, N, false><<<1, ST, 0, L.stream>>>(tab, scale, limit, grad_scale, norm);
+    const cudaError_t err = cudaGetLastError();
     launch_end(L, scale_too ? "grad_clip" : "grad_norm");
     return err;
   }
@@ -410,6 +381,9 @@ cudaError_t launch_grad_norm(const Launch &L, int n, const void *const *grads, v
   if (n <= kFewTensors)
     FNO_DISPATCH_T(dtype, err = run<T, kFewTensors>(L, n, grads, out, scale_too, sizes, grad_scale,
                                                     max_norm, norm, partial));
+  else if (n <= kSomeTensors)
+    FNO_DISPATCH_T(dtype, err = run<T, kSomeTensors>(L, n, grads, out, scale_too, sizes,
+                                                     grad_scale, max_norm, norm, partial));
   else
     FNO_DISPATCH_T(dtype, err = run<T, kClipTensors>(L, n, grads, out, scale_too, sizes,
                                                      grad_scale, max_norm, norm, partial));

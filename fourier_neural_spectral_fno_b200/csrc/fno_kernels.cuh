@@ -288,10 +288,10 @@ cudaError_t launch_ln_bwd(const Launch &L, const NormShape &s, int dtype, const 
                           void *dx, float *dgamma, float *dbeta, float *partial);
 
 // ---- gradient norm and clipping (clip.cu) ----------------------------------
-constexpr int kFewTensors = 64;      // tensors of one launch: a 2 KB parameter block,
-constexpr int kClipTensors = 1024;   // or one of 29 KB
+// tensors of one launch: a parameter block of 2, 11 or 29 KB (a launch's host time
+// grows with it, by about 3 us for the largest)
+constexpr int kFewTensors = 64, kSomeTensors = 384, kClipTensors = 1024;
 constexpr int kNormCTAs = 1184;      // most partial sums of one launch
-constexpr int kClusterChunks = 1024; // most 4 KB chunks for the one-cluster form
 // norm (device): [0] = |grad_scale| ||g||, [1] = min(1, max_norm / norm); with
 // scale_too also out[i] = grads[i] grad_scale norm[1].  partial: kNormCTAs float64
 // for each kClipTensors tensors

@@ -411,7 +411,8 @@ LISTS = {
     "many": [1 + (i * 37) % 977 for i in range(700)],
     # around the numbers of tensors and of 4 KB chunks that one launch takes
     "few": [5] * 64, "few+1": [5] * 65, "few+0": [5] * 64 + [0] * 3,
-    "one-cluster": [1 << 20], "one-cluster+1": [1 << 20, 1],
+    "one-cta": [1 << 15], "one-cta+1": [1 << 15, 1], "one-cta-many": [700] * 32,
+    "some": [1300] * 384, "some+1": [1300] * 385, "medium": [1 << 20, 1],
     "table": [1100] * 1024, "table+1": [1100] * 1025, "table+0": [1100] * 1024 + [0, 0],
     "tables": [3 + (i * 91) % 5000 for i in range(2300)],
 }
