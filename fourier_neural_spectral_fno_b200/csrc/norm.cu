@@ -209,6 +209,9 @@ cudaError_t launch_ln_fwd(const Launch &L, const NormShape &s, int dtype, const 
     return launch_ln_pipe_fwd(L, s, dtype, x, gamma, beta, y, mean, rstd);
   if (ln_rows_supported(s, dtype, false))
     return launch_ln_rows_fwd(L, s, dtype, x, gamma, beta, y, mean, rstd);
+  if (ln_odd_supported(s, dtype, false))
+    return launch_ln_odd(L, s, dtype, x, gamma, beta, nullptr, y, mean, rstd, nullptr, nullptr,
+                         nullptr, nullptr);
   if (ln_grid_supported(s, dtype, false))
     return launch_ln_grid_fwd(L, s, dtype, x, gamma, beta, y, mean, rstd);
   const long long points = s.outer * s.inner;
@@ -244,6 +247,9 @@ cudaError_t launch_ln_bwd(const Launch &L, const NormShape &s, int dtype, const 
     err = launch_ln_pipe_bwd(L, s, dtype, x, gamma, mean, rstd, dy, dx, part, &nparts);
   else if (ln_rows_supported(s, dtype, true))
     err = launch_ln_rows_bwd(L, s, dtype, x, gamma, mean, rstd, dy, dx, part, &nparts);
+  else if (ln_odd_supported(s, dtype, true))
+    err = launch_ln_odd(L, s, dtype, x, gamma, nullptr, dy, dx, nullptr, nullptr, mean, rstd,
+                        part, &nparts);
   else if (ln_grid_supported(s, dtype, true))
     err = launch_ln_grid_bwd(L, s, dtype, x, gamma, mean, rstd, dy, dx, part, &nparts);
   else

@@ -201,6 +201,14 @@ cudaError_t launch_ln_grid_bwd(const Launch &L, const NormShape &s, int dtype, c
                                const void *gamma, const float *mean, const float *rstd,
                                const void *dy, void *dx, float *partial, int *nparts);
 
+// grid layout whose rows start anywhere (norm_odd.cu); dy given: backward, outputs as
+// launch_ln_grid_bwd
+bool ln_odd_supported(const NormShape &s, int dtype, bool bwd);
+cudaError_t launch_ln_odd(const Launch &L, const NormShape &s, int dtype, const void *x,
+                          const void *gamma, const void *beta, const void *dy, void *out,
+                          float *mean_out, float *rstd_out, const float *mean_in,
+                          const float *rstd_in, float *partial, int *nparts);
+
 // rows (inner == 1), values held in registers (norm_rows.cu); outputs as above
 bool ln_rows_supported(const NormShape &s, int dtype, bool bwd);
 cudaError_t launch_ln_rows_fwd(const Launch &L, const NormShape &s, int dtype, const void *x,

@@ -100,6 +100,12 @@ SHAPES = [(1, 1, 1), (5, 3, 1), (3, 1, 7), (2, 2, 9), (7, 8, 1), (1, 20, 256), (
           (1, 520, 24), (1, 1025, 12), (2, 2100, 6), (33, 64, 1), (130, 100, 1), (9, 1000, 1),
           (4, 1001, 1), (3, 2048, 1), (5, 2052, 1), (2, 4097, 1), (2, 8192, 1), (1, 33000, 1),
           (40, 24, 2), (50, 16, 3), (3, 24, 4096), (1, 4, 100003)]
+# rows that start anywhere: every channel count the kernels round up to and its
+# neighbours, the shortest rows, rows that end inside a warp's points, rows of a
+# multiple of four values (pieces of float32, none of 16-bit gradients)
+SHAPES += [(2, 1, 257), (3, 7, 1021), (2, 8, 4099), (3, 9, 259), (1, 16, 2047), (2, 17, 385),
+           (3, 21, 449), (2, 24, 4099), (2, 25, 321), (1, 32, 4097), (5, 32, 1444), (2, 33, 513),
+           (2, 47, 767), (2, 48, 1023), (2, 49, 1025), (700, 12, 291)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
