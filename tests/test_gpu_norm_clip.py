@@ -380,6 +380,46 @@ def test_layer_norm_on_streams_and_in_a_graph(shape):
     assert all(torch.equal(o[k], want[1][k]) for k in want[1] if k != "ws")
 
 
+@pytest.mark.parametrize("dtype,shape", [("bf16", (8, 32, 1 << 16)), ("bf16", (4, 64, 1 << 16)),
+                                         ("f32", (16, 8, 1 << 16)), ("f32", (4, 64, 1 << 16))])
+def test_layer_norm_expired_wait_is_reported(dtype, shape):
+    """With the wait limit at a single probe some of the pipelines' waits give up: the
+    call reports it, and the next one with the default limit gives the same bits as
+    before."""
+    import torch
+    outer, C, inner = shape
+    g = torch.Generator(device="cuda").manual_seed(5)
+    dt = torch_dtype(dtype)
+    x, dy = (torch.randn(shape, generator=g, device="cuda").to(dt) for _ in range(2))
+    gamma = torch.ones(C, device="cuda", dtype=dt)
+    d = capi.layer_norm_desc(outer, C, inner, dtype, EPS)
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    mean, rstd = (torch.empty((outer, inner), device="cuda") for _ in range(2))
+    dg, db = (torch.empty(C, device="cuda") for _ in range(2))
+    fwd = lambda: capi.fno_layer_norm_fwd(d, x, gamma, None, y, mean, rstd)  # noqa: E731
+    bwd = lambda: capi.fno_layer_norm_bwd(d, x, gamma, mean, rstd, dy, dx, dg, db)  # noqa: E731
+    capi.fno_device_error(clear=True)
+    fwd()
+    bwd()
+    capi.fno_device_error(clear=True)
+    kept = [t.clone() for t in (y, mean, rstd, dx, dg, db)]
+    for call in (bwd, fwd) if dtype != "f32" else (bwd,):
+        prev = capi.fno_set_wait_limit(0)
+        try:
+            call()
+            torch.cuda.synchronize()
+            with pytest.raises(capi.FnoError) as info:
+                capi.fno_device_error(clear=True)
+            assert info.value.code == capi.FNO_ERR_TIMEOUT
+        finally:
+            capi.fno_set_wait_limit(prev)
+    fwd()
+    bwd()
+    capi.fno_device_error(clear=True)
+    for a, b in zip(kept, (y, mean, rstd, dx, dg, db)):
+        assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("shape", [(33, 64, 1 << 20), ((1 << 20) + 3, 2049, 1)], ids=str)
 def test_layer_norm_offsets_beyond_32_bits(shape):
     """More than 2^31 elements: the last points against the oracle, and the
