@@ -301,22 +301,6 @@ int clip_grid(const Launch &L, int chunks) {
   return ctas < cap ? ctas : cap;
 }
 
-// a launch that may begin while the one before it still runs
-template <typename... P, typename... A>
-cudaError_t launch_dependent(const Launch &L, int grid, void (*kern)(P...),
-                             const A &...args) {
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t c{};
-  c.gridDim = dim3(grid);
-  c.blockDim = dim3(CT);
-  c.stream = L.stream;
-  c.attrs = &attr;
-  c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, kern, args...);
-}
-
 template <typename T, int N>
 cudaError_t run(const Launch &L, int n, const void *const *grads, void *const *out, bool scale_too,
                 const int64_t *sizes, float grad_scale, float max_norm, float *norm,
@@ -350,7 +334,7 @@ cudaError_t run(const Launch &L, int n, const void *const *grads, void *const *o
   if (!scale_too) {
     launch_begin(L);
     const cudaError_t err =
-        launch_dependent(L, 1, k_grad_norm, (const double *)partial, nparts, scale, limit, norm);
+        launch_dependent(L, 1, CT, k_grad_norm, (const double *)partial, nparts, scale, limit, norm);
     launch_end(L, "grad_norm");
     return err;
   }
@@ -363,7 +347,7 @@ cudaError_t run(const Launch &L, int n, const void *const *grads, void *const *o
     launch_begin(L);
     const int grid = clip_grid(L, tab.first[tab.count]);
     const cudaError_t err =
-        launch_dependent(L, grid, k_grad_scale<T, N>, tab, (const double *)partial, nparts, scale,
+        launch_dependent(L, grid, CT, k_grad_scale<T, N>, tab, (const double *)partial, nparts, scale,
                          limit, grad_scale, first ? norm : nullptr);
     launch_end(L, "grad_scale");
     if (err != cudaSuccess) return err;

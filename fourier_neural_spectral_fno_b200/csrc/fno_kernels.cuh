@@ -54,6 +54,23 @@ void set_last_error(const char *fmt, ...);
 void launch_begin(const Launch &L);
 void launch_end(const Launch &L, const char *tag);
 
+// A launch that may begin while the one before it still runs: the kernel waits for
+// that one's results with cudaGridDependencySynchronize.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(const Launch &L, unsigned grid, unsigned threads, void (*kern)(P...),
+                             const A &...args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(grid);
+  c.blockDim = dim3(threads);
+  c.stream = L.stream;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kern, args...);
+}
+
 // ---- forward truncated transform (S0-S2) ----------------------------------
 // in0 (and in1 for LOAD_DZ) are [B][C][N]; out xhat [B][C][K] float2.
 // zpart scratch: fwd_zpart_floats() floats.

@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(MW ? 32 * MW : GT)
                   float inv_c) {
   constexpr int LP = Lanes<T, V>::LP, G = Lanes<T, V>::G, P = LP * V;
   __shared__ float red[MW ? 2 * MW * P : 2 * (GT / 32) * CPL * G];
+  cudaTriggerProgrammaticLaunchCompletion();   // the sum of the partial rows is set up meanwhile
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int pl = lane % LP, grp = lane / LP;
   const int c0 = MW ? warp * G + grp : grp, step = MW ? warps * G : G;

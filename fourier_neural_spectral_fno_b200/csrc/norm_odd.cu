@@ -12,7 +12,7 @@
 // memory, took 48 instructions a value.  Copying a tile's whole 16-byte pieces
 // through shared memory, each row at its own offset, measured slower (29 us at 12 x
 // 20 x 48323 float16).  Measured there, against the element kernels: forward 14.2
-// and 19.6 us, backward 27.8 and 41.2; float32 19.2 and 19.5, 32.0 and 37.6.
+// and 19.6 us, backward 24.4 and 38; float32 19.2 and 19.5, 28.8 and 34.
 #include "norm_common.cuh"
 
 namespace fno {
@@ -130,6 +130,7 @@ template <typename T, int CM, int CLO>
 __global__ void __launch_bounds__(OT) k_ln_bwd_odd(const __grid_constant__ OddArgs a) {
   __shared__ float2 coef[CM];
   __shared__ float red[OT / 32][2 * CM];
+  cudaTriggerProgrammaticLaunchCompletion();   // the sum of the partial rows is set up meanwhile
   coefs<T>(a, coef);
   const int C = a.C, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float dg[CM], db[CM];

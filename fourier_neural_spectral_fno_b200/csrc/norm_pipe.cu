@@ -385,6 +385,7 @@ __global__ void __launch_bounds__(S::threads, 1)
                   const __grid_constant__ CUtensorMap mdx, const __grid_constant__ PipeArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   constexpr int N = S::N;
+  cudaTriggerProgrammaticLaunchCompletion();   // the sum of the partial rows is set up meanwhile
   Cursor at;
   Walk<S> w = pipe_begin<S>(smem, a, &mx, &mdy, &mdx, at);
   const float4 *coef = reinterpret_cast<const float4 *>(smem + S::coef) + w.part;

@@ -272,6 +272,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS)
   constexpr int V = Rows<T>::V, H = V / 2;
   extern __shared__ float acc[];   // [groups][C][2], where a CTA has several
   __shared__ float red[512];
+  cudaTriggerProgrammaticLaunchCompletion();   // the sum of the partial rows is set up meanwhile
   Group gr{red, tpr, (int)(threadIdx.x & (tpr - 1)), (int)(threadIdx.x / tpr), 0};
   const int R = blockDim.x / tpr;
   const long long G = (long long)gridDim.x * R, first = (long long)blockIdx.x * R + gr.r;
