@@ -1,4 +1,4 @@
-// Layer norm over the channels of grid activations as a TMA pipeline: at most 64
+// Layer norm over the channels of grid activations as a TMA pipeline: at most 128
 // channels, grids whose rows start on 16-byte boundaries.
 //
 // A team of warps is a pipeline of its own.  Its tile is every channel of SG
@@ -20,7 +20,8 @@
 // box is CM rows high.  Rows beyond C are filled with zeros, which add nothing to
 // the backward's sums (the forward's squares leave them out), and are not stored.
 //
-// Bound by HBM; see the measured figures at the launchers.
+// Bound by HBM: 32 x 64 x 65536 bfloat16 backward 128.7 us with its parameters'
+// sums, 99 % of the copy rate; 2 x 20 x 128^3 float32 172.5 us, 93 %.
 #include <cuda.h>
 
 #include "norm_common.cuh"
@@ -284,15 +285,17 @@ __device__ __forceinline__ Walk<S> pipe_begin(unsigned char *smem, const PipeArg
   return w;
 }
 
-// 16-bit types.  The converted values stay in registers from the first sweep on
-// (a word is read and converted once); a value's own step is at least 2^13 times
-// the rounding of the mean, which float32's correction (norm.cu) is there for.
+// The converted values stay in registers from the first sweep on (a word is read
+// and converted once).  float32's correction of the mean (norm.cu): a 16-bit value's
+// own step is at least 2^13 times the mean's rounding, so these types leave it out.
 template <typename S>
 __global__ void __launch_bounds__(S::threads, 1)
     k_ln_fwd_pipe(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my,
                   const __grid_constant__ PipeArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   constexpr int N = S::N;
+  constexpr bool kCorrect = S::E == 1;
+  constexpr int M = kCorrect ? 2 * N : N;   // sums of the second sweep
   Cursor at;
   Walk<S> w = pipe_begin<S>(smem, a, &mx, nullptr, &my, at);
   const float4 *coef = reinterpret_cast<const float4 *>(smem + S::coef) + w.part;
@@ -306,8 +309,8 @@ __global__ void __launch_bounds__(S::threads, 1)
     }
     unsigned char *tile = w.ring + (at.it % S::NS) * S::stage;
     unsigned char *st = tile + 2 * w.part * S::row + w.col * S::column + w.lane * 4;
-    f32x2 v[S::pairs][N], s[N], m[N];
-    float sum[N];
+    f32x2 v[S::pairs][N], s[N], e[N], m[N];
+    float sum[M];
 #pragma unroll
     for (int k = 0; k < N; ++k) s[k] = f2splat(0.f);
 #pragma unroll
@@ -328,7 +331,7 @@ __global__ void __launch_bounds__(S::threads, 1)
     for (int k = 0; k < N; ++k) {
       mean[k] = sum[k] * a.inv_c;
       m[k] = f2splat(-mean[k]);
-      s[k] = f2splat(0.f);
+      s[k] = e[k] = f2splat(0.f);
     }
 #pragma unroll
     for (int i = 0; i < S::pairs; ++i) {
@@ -341,26 +344,40 @@ __global__ void __launch_bounds__(S::threads, 1)
           f2unpack(v[i][k], d0, d1);
           v[i][k] = f2pack(c < C ? d0 : 0.f, c + 1 < C ? d1 : 0.f);
         }
+        if (kCorrect) e[k] = f2add(e[k], v[i][k]);
         s[k] = f2fma(v[i][k], v[i][k], s[k]);
       }
     }
 #pragma unroll
-    for (int k = 0; k < N; ++k) sum[k] = pair_sum(s[k]);
-    w.template exchange<N>(sum, turn++, true);
+    for (int k = 0; k < N; ++k) {
+      sum[k] = pair_sum(s[k]);
+      if (kCorrect) sum[N + k] = pair_sum(e[k]);
+    }
+    w.template exchange<M>(sum, turn++, true);
     const long long n = (long long)at.seg * S::P + (w.col * 32 * S::W + w.lane) * S::E;
     float r[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      r[k] = ln_rstd(sum[k] * a.inv_c, 0.f, a.eps);
+      const float ek = kCorrect ? sum[N + k] * a.inv_c : 0.f;
+      r[k] = ln_rstd(sum[k] * a.inv_c, ek, a.eps);
       m[k] = f2splat(r[k]);
+      if (kCorrect) {
+        mean[k] += ek;
+        e[k] = f2splat(-ek);
+      }
     }
     if (a.mean_out && w.part == 0) {
 #pragma unroll
       for (int k = 0; k < S::W; ++k)
-        if (n + 64 * k < a.inner) {   // two points of a word
-          const long long p = at.b * a.inner + n + 64 * k;
-          *reinterpret_cast<float2 *>(a.mean_out + p) = make_float2(mean[2 * k], mean[2 * k + 1]);
-          *reinterpret_cast<float2 *>(a.rstd_out + p) = make_float2(r[2 * k], r[2 * k + 1]);
+        if (n + 32 * S::E * k < a.inner) {   // the points of a word
+          const long long p = at.b * a.inner + n + 32 * S::E * k;
+          if constexpr (S::E == 2) {
+            *reinterpret_cast<float2 *>(a.mean_out + p) = make_float2(mean[2 * k], mean[2 * k + 1]);
+            *reinterpret_cast<float2 *>(a.rstd_out + p) = make_float2(r[2 * k], r[2 * k + 1]);
+          } else {
+            a.mean_out[p] = mean[k];
+            a.rstd_out[p] = r[k];
+          }
         }
     }
 #pragma unroll
@@ -368,7 +385,10 @@ __global__ void __launch_bounds__(S::threads, 1)
       const float4 gb = coef[S::KW * i];
       const f32x2 ga = f2pack(gb.x, gb.y), be = f2pack(gb.z, gb.w);
 #pragma unroll
-      for (int k = 0; k < N; ++k) v[i][k] = f2fma(f2mul(v[i][k], m[k]), ga, be);
+      for (int k = 0; k < N; ++k) {
+        if (kCorrect) v[i][k] = f2add(v[i][k], e[k]);
+        v[i][k] = f2fma(f2mul(v[i][k], m[k]), ga, be);
+      }
       st_pairs<S>(st + 2 * S::KW * i * S::row, v[i]);
     }
     w.store(at, tile);
@@ -582,14 +602,19 @@ cudaError_t bwd_t(const Launch &L, const NormShape &s, const void *x, const void
 // Per channel count: CM, words per lane, warps per column, columns per tile, most
 // teams; chosen by a sweep over these at 64 M (32-bit) and 128 M bytes (16-bit)
 // per array.  Rows of 512 bytes and one or two columns' worth of warps per team
-// were best nearly everywhere; the neighbours are within 5 %.
+// were best nearly everywhere, the neighbours within 5 %; above 64 channels tiles
+// that leave room for two teams (8 x 100 x 65536 bfloat16: forward 39.1 us with two
+// teams of two columns, 42.7 with one of four; 16 warps a column 95 us backward,
+// four 63).
 struct Cfg {
   int cm, w, kw, sg, mt;
 };
 constexpr Cfg kFwd[] = {{8, 2, 1, 2, 12}, {16, 2, 1, 2, 8}, {20, 2, 1, 2, 6}, {24, 2, 1, 2, 6},
-                        {32, 1, 1, 4, 4}, {48, 1, 4, 4, 2}, {64, 1, 4, 4, 2}};
+                        {32, 1, 1, 4, 4}, {48, 1, 4, 4, 2}, {64, 1, 4, 4, 2}, {96, 1, 4, 2, 2},
+                        {128, 1, 4, 2, 2}};
 constexpr Cfg kBwd[] = {{8, 2, 1, 2, 8}, {16, 2, 2, 2, 4}, {20, 2, 2, 2, 3}, {24, 2, 2, 2, 3},
-                        {32, 1, 2, 2, 4}, {48, 1, 4, 2, 3}, {64, 1, 4, 2, 2}};
+                        {32, 1, 2, 2, 4}, {48, 1, 4, 2, 3}, {64, 1, 4, 2, 2}, {96, 1, 4, 1, 2},
+                        {128, 1, 4, 1, 2}};
 template <typename T, int I, int ARRAYS> struct ShapeOf {
   static constexpr Cfg c = ARRAYS == 1 ? kFwd[I] : kBwd[I];
   static constexpr int lo = I ? kFwd[I ? I - 1 : 0].cm + 1 : 1;
@@ -604,26 +629,32 @@ template <typename T, int I, int ARRAYS> struct ShapeOf {
     else if (s.C <= 24) CALL(3);     \
     else if (s.C <= 32) CALL(4);     \
     else if (s.C <= 48) CALL(5);     \
-    else CALL(6);                    \
+    else if (s.C <= 64) CALL(6);     \
+    else if (s.C <= 96) CALL(7);     \
+    else CALL(8);                    \
   } while (0)
 
 }  // namespace
 
-// Rows on 16-byte boundaries (the maps' strides), at most 64 channels, tile
+// Rows on 16-byte boundaries (the maps' strides), at most 128 channels, tile
 // numbers of 31 bits, strides the maps can hold; rows that fill most of their
 // tiles of up to 256 points; and enough work that the pipelines' start does not
-// show.  Against the register kernels (norm_grid.cu),
-// us: backward float32 20 x 4096 at batch 8 / 16 / 32: 6.7 / 8.4 / 11.9 against
+// show.  Against the register kernels (norm_grid.cu), us, with up to 64 channels:
+// backward float32 20 x 4096 at batch 8 / 16 / 32: 6.7 / 8.4 / 11.9 against
 // 5.9 / 8.5 / 12.1, 64 x 4096 at 2 / 4: 6.4 / 7.3 against 6.4 / 9.0; bfloat16
 // 20 x 4096 at 8 / 16: 7.4 / 7.2 against 7.8 / 10.2: from a million values on.
 // Forward bfloat16 20 x 4096 at 32 / 64: 5.2 / 7.1 against 4.5 / 7.7: from four
-// million.  The float32 forward stays with the register kernels at every size
-// (16 x 32 x 65536: 44.8 us, 96 % of the copy rate, against 51).
+// million; float32 never (16 x 32 x 65536: 51 against 44.8, 96 % of the copy rate).
+// With more channels, where the register kernels split a point's channels over a
+// CTA's warps, from a million values on in every direction and type: at 128 x 4096,
+// batch 4, and 128 x 65536, batch 8, forward bfloat16 5.4 and 49.9 against 7.2 and
+// 74.6, float32 5.1 and 97.5 against 8.6 and 112; backward bfloat16 7.4 and 70.3
+// against 7.9 and 139, float32 8.8 and 130 against 10.8 and 208.
 bool ln_pipe_supported(const NormShape &s, int dtype, bool bwd) {
-  if (!bwd && dtype == DT_F32) return false;
+  if (!bwd && dtype == DT_F32 && s.C <= 64) return false;
   const long long es = dtype == DT_F32 ? 4 : 2, n = s.outer * s.C * s.inner;
-  if (s.C > 64 || s.inner * es % 16 != 0 || (s.inner < 512 && s.inner != 256) ||
-      n < (bwd ? 1 << 20 : 1 << 22))
+  if (s.C > 128 || s.inner * es % 16 != 0 || (s.inner < 512 && s.inner != 256) ||
+      n < (bwd || s.C > 64 ? 1 << 20 : 1 << 22))
     return false;
   const long long segs = (s.inner + 31) / 32;
   return s.inner <= 0x7fffffffLL && s.outer <= 0x7fffffffLL / segs && n * es < (1LL << 40);
@@ -644,9 +675,13 @@ cudaError_t launch_ln_pipe_fwd(const Launch &L, const NormShape &s, int dtype, c
   if (dtype == DT_F16) {
     using T = __half;
     LN_PIPE_CASES(LN_FWD);
-  } else {
+  } else if (dtype == DT_BF16) {
     using T = __nv_bfloat16;
     LN_PIPE_CASES(LN_FWD);
+  } else {
+    using T = float;
+    if (s.C <= 96) LN_FWD(7);
+    else LN_FWD(8);
   }
   launch_end(L, "ln_fwd_pipe");
 #undef LN_FWD

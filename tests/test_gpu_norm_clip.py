@@ -145,7 +145,8 @@ def _check_large(got, ref, tol, what):
 # tile, one sample and many, one tile per sample
 LARGE = [(3, 5, 281000), (17, 8, 33000), (2, 13, 163848), (5, 16, 53000), (1, 17, 250008),
          (3, 20, 70008), (4, 23, 46000), (7, 24, 25000), (2, 31, 68008), (540, 32, 256),
-         (3, 45, 31512), (2, 48, 44000), (3, 61, 23000), (2, 64, 33000), (130, 64, 520)]
+         (3, 45, 31512), (2, 48, 44000), (3, 61, 23000), (2, 64, 33000), (130, 64, 520),
+         (4, 65, 16392), (2, 96, 9000), (1, 97, 40008), (3, 127, 5000), (33, 128, 256)]
 
 
 @pytest.mark.parametrize("shape", LARGE, ids=str)
@@ -246,7 +247,8 @@ def test_layer_norm_optional_arguments_and_in_place(shape):
 
 
 @pytest.mark.parametrize("shape", [(2, 20, 64), (2, 20, 35), (8, 64, 1), (4, 1001, 1),
-                                   (1, 1100, 8), (1, 33001, 1), (2, 200, 16)], ids=str)
+                                   (1, 1100, 8), (1, 33001, 1), (2, 200, 16), (2, 20, 1023),
+                                   (4, 96, 4096), (1, 128, 8196)], ids=str)
 def test_layer_norm_large_offset(shape):
     """A common offset of 4096 against a spread of one: the tolerances hold
     unchanged (for the mean they grow with the values' size), because the
@@ -262,6 +264,42 @@ def test_layer_norm_large_offset(shape):
     mean, rstd = torch.empty(outer, inner, device="cuda"), torch.empty(outer, inner, device="cuda")
     capi.fno_layer_norm_fwd(d, _dev(x), _dev(gamma), _dev(beta), y, mean, rstd)
     _check_fwd(y, mean, rstd, x, gamma, beta, "f32")
+
+
+@pytest.mark.parametrize("shape", [(2, 20, 1023), (3, 32, 4099), (2, 48, 777), (4, 96, 4096),
+                                   (2, 128, 4104), (9, 32, 16384)], ids=str)
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_layer_norm_non_finite_grid_points_stay_alone(shape, dtype):
+    """One point's NaN or infinity makes that point NaN in y, dx and dgamma, and
+    leaves every other point of y and dx, and dbeta, as they were."""
+    import torch
+    outer, C, inner = shape
+    g = torch.Generator(device="cuda").manual_seed(31)
+    dt = torch_dtype(dtype)
+    x, dy = (torch.randn(shape, generator=g, device="cuda").to(dt) for _ in range(2))
+    gamma = (1 + 0.2 * torch.randn(C, generator=g, device="cuda")).to(dt)
+    d = capi.layer_norm_desc(outer, C, inner, dtype, EPS)
+
+    def both(v):
+        y, dx = torch.empty_like(v), torch.empty_like(v)
+        mean, rstd = (torch.empty((outer, inner), device="cuda") for _ in range(2))
+        dg, db = (torch.empty(C, device="cuda") for _ in range(2))
+        capi.fno_layer_norm_fwd(d, v, gamma, None, y, mean, rstd)
+        capi.fno_layer_norm_bwd(d, v, gamma, mean, rstd, dy, dx, dg, db)
+        return y, dx, dg, db
+
+    y, dx, dg, db = both(x)
+    assert bool(torch.isfinite(dg).all())
+    for bad in (np.nan, np.inf, -np.inf):
+        for b, at in ((0, 0), (outer - 1, inner - 1), (outer // 2, inner // 2)):
+            z = x.clone()
+            z[b, C // 3, at] = bad
+            y2, dx2, dg2, db2 = both(z)
+            for got, clean in ((y2, y), (dx2, dx)):
+                assert bool(torch.isnan(got[b, :, at]).all())
+                got[b, :, at] = clean[b, :, at]
+                assert torch.equal(got, clean)
+            assert bool(torch.isnan(dg2).all()) and torch.equal(db2, db)
 
 
 @pytest.mark.parametrize("shape", [(2, 20, 64), (2, 20, 35), (8, 64, 1), (4, 1001, 1),
