@@ -12,7 +12,8 @@
 // memory, took 48 instructions a value.  Copying a tile's whole 16-byte pieces
 // through shared memory, each row at its own offset, measured slower (29 us at 12 x
 // 20 x 48323 float16).  Measured there, against the element kernels: forward 14.2
-// and 19.6 us, backward 24.4 and 38; float32 19.2 and 19.5, 28.8 and 34.
+// and 19.6 us, backward 27.8 and 41.2; float32 19.2 and 19.5, 32.1 and 37.5 (backward
+// with a sum of the partial rows that took 3 us more than now).
 #include "norm_common.cuh"
 
 namespace fno {
