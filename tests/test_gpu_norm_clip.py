@@ -105,7 +105,10 @@ SHAPES = [(1, 1, 1), (5, 3, 1), (3, 1, 7), (2, 2, 9), (7, 8, 1), (1, 20, 256), (
 # multiple of four values (pieces of float32, none of 16-bit gradients)
 SHAPES += [(2, 1, 257), (3, 7, 1021), (2, 8, 4099), (3, 9, 259), (1, 16, 2047), (2, 17, 385),
            (3, 21, 449), (2, 24, 4099), (2, 25, 321), (1, 32, 4097), (5, 32, 1444), (2, 33, 513),
-           (2, 47, 767), (2, 48, 1023), (2, 49, 1025), (700, 12, 291)]
+           (2, 47, 767), (2, 48, 1023), (2, 49, 1025), (700, 12, 291), (2, 40, 1444),
+           (1, 57, 4099), (3, 64, 289), (2, 65, 257), (1, 73, 1021), (2, 81, 259), (2, 96, 517),
+           (3, 97, 345), (2, 105, 299), (1, 113, 777), (1, 128, 2049), (2, 129, 301),
+           (650, 33, 257)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
@@ -248,7 +251,7 @@ def test_layer_norm_optional_arguments_and_in_place(shape):
 
 @pytest.mark.parametrize("shape", [(2, 20, 64), (2, 20, 35), (8, 64, 1), (4, 1001, 1),
                                    (1, 1100, 8), (1, 33001, 1), (2, 200, 16), (2, 20, 1023),
-                                   (4, 96, 4096), (1, 128, 8196)], ids=str)
+                                   (2, 77, 1023), (4, 96, 4096), (1, 128, 8196)], ids=str)
 def test_layer_norm_large_offset(shape):
     """A common offset of 4096 against a spread of one: the tolerances hold
     unchanged (for the mean they grow with the values' size), because the
@@ -266,7 +269,7 @@ def test_layer_norm_large_offset(shape):
     _check_fwd(y, mean, rstd, x, gamma, beta, "f32")
 
 
-@pytest.mark.parametrize("shape", [(2, 20, 1023), (3, 32, 4099), (2, 48, 777), (4, 96, 4096),
+@pytest.mark.parametrize("shape", [(2, 20, 1023), (3, 32, 4099), (2, 48, 777), (2, 97, 777), (4, 96, 4096),
                                    (2, 128, 4104), (9, 32, 16384)], ids=str)
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 def test_layer_norm_non_finite_grid_points_stay_alone(shape, dtype):
