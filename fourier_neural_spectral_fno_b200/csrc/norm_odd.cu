@@ -98,10 +98,8 @@ template <int KW> __device__ __forceinline__ int first_channel(int C, int warp) 
 // CLO: the fewest channels of a warp that CM is used for
 template <typename T, int CM, int CLO, int PPL, int KW>
 __global__ void __launch_bounds__(odd_threads(KW)) k_ln_fwd_odd(const __grid_constant__ OddArgs a) {
-  constexpr bool kCorrect = sizeof(T) == 4;   // as in norm_pipe.cu
-  constexpr int M = kCorrect ? 2 * PPL : PPL;
   __shared__ float2 coef[CM * KW];
-  __shared__ float sums[1][KW][PPL][32], sums2[1][KW][M][32];
+  __shared__ float sums[1][KW][PPL][32], sums2[1][KW][2 * PPL][32];
   coefs<T>(a, CM * KW, coef);
   const int warp = threadIdx.x >> 5, c0 = first_channel<KW>(a.C, warp);
   const unsigned tile = KW > 1 ? blockIdx.x : blockIdx.x * (OT / 32) + warp;
@@ -134,21 +132,21 @@ __global__ void __launch_bounds__(odd_threads(KW)) k_ln_fwd_odd(const __grid_con
 #pragma unroll
       for (int k = 0; k < PPL; ++k) {
         v[c][k] -= m[k];
-        if (kCorrect) e[k] += v[c][k];
+        e[k] += v[c][k];
         q[k] = fmaf(v[c][k], v[c][k], q[k]);
       }
   if (KW > 1) {
-    float qe[M];
+    float qe[2 * PPL];
 #pragma unroll
     for (int k = 0; k < PPL; ++k) {
       qe[k] = q[k];
-      if (kCorrect) qe[PPL + k] = e[k];
+      qe[PPL + k] = e[k];
     }
-    join<KW, M>(sums2, 0, qe);
+    join<KW, 2 * PPL>(sums2, 0, qe);
 #pragma unroll
     for (int k = 0; k < PPL; ++k) {
       q[k] = qe[k];
-      if (kCorrect) e[k] = qe[PPL + k];
+      e[k] = qe[PPL + k];
     }
   }
   T *p = static_cast<T *>(a.out) + base;
@@ -167,10 +165,8 @@ __global__ void __launch_bounds__(odd_threads(KW)) k_ln_fwd_odd(const __grid_con
     if (c < CLO || c < C) {
       const float2 gb = coef[c0 + c];
 #pragma unroll
-      for (int k = 0; k < PPL; ++k) {
-        const float d = kCorrect ? v[c][k] - e[k] : v[c][k];
-        if (sp.in[k]) p[sp.off[k]] = from_f<T>(fmaf(d * q[k], gb.x, gb.y));
-      }
+      for (int k = 0; k < PPL; ++k)
+        if (sp.in[k]) p[sp.off[k]] = from_f<T>(fmaf((v[c][k] - e[k]) * q[k], gb.x, gb.y));
     }
     p += hop;
   }

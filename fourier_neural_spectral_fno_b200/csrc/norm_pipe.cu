@@ -286,16 +286,14 @@ __device__ __forceinline__ Walk<S> pipe_begin(unsigned char *smem, const PipeArg
 }
 
 // The converted values stay in registers from the first sweep on (a word is read
-// and converted once).  float32's correction of the mean (norm.cu): a 16-bit value's
-// own step is at least 2^13 times the mean's rounding, so these types leave it out.
+// and converted once).  The correction of the mean (norm.cu) serves the 16-bit types
+// as well: a point of equal values has no step of its own to outweigh the rounding.
 template <typename S>
 __global__ void __launch_bounds__(S::threads, 1)
     k_ln_fwd_pipe(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my,
                   const __grid_constant__ PipeArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   constexpr int N = S::N;
-  constexpr bool kCorrect = S::E == 1;
-  constexpr int M = kCorrect ? 2 * N : N;   // sums of the second sweep
   Cursor at;
   Walk<S> w = pipe_begin<S>(smem, a, &mx, nullptr, &my, at);
   const float4 *coef = reinterpret_cast<const float4 *>(smem + S::coef) + w.part;
@@ -310,7 +308,7 @@ __global__ void __launch_bounds__(S::threads, 1)
     unsigned char *tile = w.ring + (at.it % S::NS) * S::stage;
     unsigned char *st = tile + 2 * w.part * S::row + w.col * S::column + w.lane * 4;
     f32x2 v[S::pairs][N], s[N], e[N], m[N];
-    float sum[M];
+    float sum[2 * N];
 #pragma unroll
     for (int k = 0; k < N; ++k) s[k] = f2splat(0.f);
 #pragma unroll
@@ -344,27 +342,25 @@ __global__ void __launch_bounds__(S::threads, 1)
           f2unpack(v[i][k], d0, d1);
           v[i][k] = f2pack(c < C ? d0 : 0.f, c + 1 < C ? d1 : 0.f);
         }
-        if (kCorrect) e[k] = f2add(e[k], v[i][k]);
+        e[k] = f2add(e[k], v[i][k]);
         s[k] = f2fma(v[i][k], v[i][k], s[k]);
       }
     }
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       sum[k] = pair_sum(s[k]);
-      if (kCorrect) sum[N + k] = pair_sum(e[k]);
+      sum[N + k] = pair_sum(e[k]);
     }
-    w.template exchange<M>(sum, turn++, true);
+    w.template exchange<2 * N>(sum, turn++, true);
     const long long n = (long long)at.seg * S::P + (w.col * 32 * S::W + w.lane) * S::E;
     float r[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      const float ek = kCorrect ? sum[N + k] * a.inv_c : 0.f;
+      const float ek = sum[N + k] * a.inv_c;
       r[k] = ln_rstd(sum[k] * a.inv_c, ek, a.eps);
       m[k] = f2splat(r[k]);
-      if (kCorrect) {
-        mean[k] += ek;
-        e[k] = f2splat(-ek);
-      }
+      mean[k] += ek;
+      e[k] = f2splat(-ek);
     }
     if (a.mean_out && w.part == 0) {
 #pragma unroll
@@ -386,8 +382,7 @@ __global__ void __launch_bounds__(S::threads, 1)
       const f32x2 ga = f2pack(gb.x, gb.y), be = f2pack(gb.z, gb.w);
 #pragma unroll
       for (int k = 0; k < N; ++k) {
-        if (kCorrect) v[i][k] = f2add(v[i][k], e[k]);
-        v[i][k] = f2fma(f2mul(v[i][k], m[k]), ga, be);
+        v[i][k] = f2fma(f2mul(f2add(v[i][k], e[k]), m[k]), ga, be);
       }
       st_pairs<S>(st + 2 * S::KW * i * S::row, v[i]);
     }

@@ -125,7 +125,6 @@ __global__ void __launch_bounds__(THREADS)
                   float *__restrict__ mean, float *__restrict__ rstd, long long rows, int C,
                   int tpr, float inv_c, float eps) {
   constexpr int V = Rows<T>::V, H = V / 2;
-  constexpr bool kCorrect = sizeof(T) == 4;   // as in norm_pipe.cu
   __shared__ float red[512];
   Group gr{red, tpr, (int)(threadIdx.x & (tpr - 1)), (int)(threadIdx.x / tpr), 0};
   const int R = blockDim.x / tpr;
@@ -167,12 +166,12 @@ __global__ void __launch_bounds__(THREADS)
       for (int i = 0; i < H; ++i) {
         v[j][i] = f2add(v[j][i], m);
         if (!whole) v[j][i] = masked(v[j][i], lo + 2 * i, C);
-        if (kCorrect) e[i & 1] = f2add(e[i & 1], v[j][i]);
+        e[i & 1] = f2add(e[i & 1], v[j][i]);
         s[i & 1] = f2fma(v[j][i], v[j][i], s[i & 1]);
       }
     }
-    float q[2] = {pair_sum(f2add(s[0], s[1])), kCorrect ? pair_sum(f2add(e[0], e[1])) : 0.f};
-    gr.sum<kCorrect ? 2 : 1>(q);
+    float q[2] = {pair_sum(f2add(s[0], s[1])), pair_sum(f2add(e[0], e[1]))};
+    gr.sum<2>(q);
     const float ek = q[1] * inv_c, r = ln_rstd(q[0] * inv_c, ek, eps);
     if (row < rows) {
       if (mean && gr.t == 0) {
@@ -183,10 +182,8 @@ __global__ void __launch_bounds__(THREADS)
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
 #pragma unroll
-        for (int i = 0; i < H; ++i) {
-          if (kCorrect) v[j][i] = f2add(v[j][i], em);
-          v[j][i] = f2fma(f2mul(v[j][i], rr), ga[j][i], be[j][i]);
-        }
+        for (int i = 0; i < H; ++i)
+          v[j][i] = f2fma(f2mul(f2add(v[j][i], em), rr), ga[j][i], be[j][i]);
         store_piece<T, SHIFT>(v[j], y + row * C, lo0 + j * hop, C);
       }
     }
@@ -202,7 +199,6 @@ __global__ void __launch_bounds__(THREADS, (NV <= 4 ? 1280 : 1024) / THREADS)
                          T *y, float *__restrict__ mean, float *__restrict__ rstd, long long rows,
                          int C, int tpr, float inv_c, float eps) {
   constexpr int V = Rows<T>::V, H = V / 2;
-  constexpr bool kCorrect = sizeof(T) == 4;   // as in norm_pipe.cu
   __shared__ float red[512];
   Group gr{red, tpr, (int)(threadIdx.x & (tpr - 1)), (int)(threadIdx.x / tpr), 0};
   const long long row = (long long)blockIdx.x * (THREADS / tpr) + gr.r;
@@ -231,14 +227,14 @@ __global__ void __launch_bounds__(THREADS, (NV <= 4 ? 1280 : 1024) / THREADS)
 #pragma unroll
       for (int i = 0; i < H; ++i) {
         v[i] = f2add(v[i], m);
-        if (kCorrect) e[i & 1] = f2add(e[i & 1], v[i]);
+        e[i & 1] = f2add(e[i & 1], v[i]);
         s[i & 1] = f2fma(v[i], v[i], s[i & 1]);
       }
       p[j].keep();
     }
   }
-  float q[2] = {pair_sum(f2add(s[0], s[1])), kCorrect ? pair_sum(f2add(e[0], e[1])) : 0.f};
-  gr.sum<kCorrect ? 2 : 1>(q);
+  float q[2] = {pair_sum(f2add(s[0], s[1])), pair_sum(f2add(e[0], e[1]))};
+  gr.sum<2>(q);
   const float ek = q[1] * inv_c, r = ln_rstd(q[0] * inv_c, ek, eps);
   if (row >= rows) return;
   if (mean && gr.t == 0) {
@@ -256,8 +252,7 @@ __global__ void __launch_bounds__(THREADS, (NV <= 4 ? 1280 : 1024) / THREADS)
       p[j].get2(v);
 #pragma unroll
       for (int i = 0; i < H; ++i) {
-        v[i] = f2add(v[i], m);
-        if (kCorrect) v[i] = f2add(v[i], em);
+        v[i] = f2add(f2add(v[i], m), em);
         v[i] = f2fma(f2mul(v[i], rr), ga[i], be[i]);
       }
       store_piece<T, false>(v, y + row * C, lo, C);
