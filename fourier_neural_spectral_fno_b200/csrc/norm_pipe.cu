@@ -393,7 +393,8 @@ __global__ void __launch_bounds__(S::threads, 1)
 
 // Per point: first sweep c1 = sum g, c2 = sum g xh (g = dy gamma) and the
 // channels' dgamma += dy xh, dbeta += dy in registers; second sweep
-//   dx = (dy (gamma rstd) - rstd c1 / C) - (x - mean) rstd^2 c2 / C
+//   dx = rstd ((g - c1 / C) - xh c2 / C)
+// (rstd^2 c2 / C, one product less, leaves float32's range long before dx does)
 template <typename S>
 __global__ void __launch_bounds__(S::threads, 1)
     k_ln_bwd_pipe(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mdy,
@@ -481,10 +482,8 @@ __global__ void __launch_bounds__(S::threads, 1)
     }
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      float rk, unused;
-      f2unpack(rr[k], rk, unused);
-      c1[k] = f2splat(-rk * (sums[2 * k] * a.inv_c));
-      c2[k] = f2splat(-rk * rk * (sums[2 * k + 1] * a.inv_c));
+      c1[k] = f2splat(-(sums[2 * k] * a.inv_c));
+      c2[k] = f2splat(-(sums[2 * k + 1] * a.inv_c));
     }
 #pragma unroll
     for (int i = 0; i < S::pairs; ++i) {
@@ -494,8 +493,10 @@ __global__ void __launch_bounds__(S::threads, 1)
       const float4 gb = coef[S::KW * i];
       const f32x2 ga = f2pack(gb.x, gb.y);
 #pragma unroll
-      for (int k = 0; k < N; ++k)
-        x[k] = f2fma(f2add(x[k], m[k]), c2[k], f2fma(y[k], f2mul(ga, rr[k]), c1[k]));
+      for (int k = 0; k < N; ++k) {
+        const f32x2 xh = f2mul(f2add(x[k], m[k]), rr[k]);
+        x[k] = f2mul(f2fma(xh, c2[k], f2fma(y[k], ga, c1[k])), rr[k]);
+      }
       st_pairs<S>(sy + 2 * S::KW * i * S::row, x);
     }
     w.store(now, tile + S::array);

@@ -1,5 +1,5 @@
-"""Layer norm where its accuracy or its coverage could get lost: points without
-spread.
+"""Layer norm where its accuracy could get lost: points without spread, values far
+from one.
 
 Tolerances.  u = 2^-24 is half a float32 step; a storage rounding is off by at
 most finfo(t).eps / 2 of the value (and by half the smallest subnormal).
@@ -102,3 +102,37 @@ def test_layer_norm_points_of_one_step(shape, dtype):
     tol = (2 * C + 16) * U * (1 + xh.abs()) * ga.abs() + 4 * U * ry.abs()
     tol = tol + HALF[dtype] * (ry.abs() + tol) + TINY[dtype]
     assert bool(((y.double() - ry).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("shape", [(3, 20, 70008), (2, 64, 33000), (1, 97, 40008), (33, 128, 256),
+                                   (2, 20, 1023), (2, 65, 257), (3, 32, 64), (2, 200, 16),
+                                   (9, 56, 1), (4, 1001, 1), (2, 300, 40), (1, 33000, 1)], ids=str)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("spread,size,eps", [(2.0 ** 50, 2.0 ** -35, 1e-5), (2.0 ** -60, 2.0 ** 12, 1e-37)],
+                         ids=["wide", "narrow"])
+def test_layer_norm_backward_far_from_one(shape, dtype, spread, size, eps):
+    """x of spread 2^50 with dy of 2^-35, and of spread 2^-60 with dy of 2^12: dx, 2^-85
+    and 2^72, lies well inside the type's range, as do xh, g and the means of g and g xh;
+    so dx is off by rstd (C + 16) u (|g| + mean|g| + |xh| mean|g xh|) and its rounding to
+    storage, as everywhere else."""
+    import torch
+    outer, C, inner = shape
+    g = torch.Generator(device="cuda").manual_seed(53)
+    dt = torch_dtype(dtype)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    x, dy = (spread * rnd(*shape)).to(dt), (size * rnd(*shape)).to(dt)
+    gamma = (1 + 0.2 * rnd(C)).to(dt)
+    d = capi.layer_norm_desc(outer, C, inner, dtype, eps)
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    mean, rstd = (torch.empty((outer, inner), device="cuda") for _ in range(2))
+    dg, db = (torch.empty(C, device="cuda") for _ in range(2))
+    capi.fno_layer_norm_fwd(d, x, gamma, None, y, mean, rstd)
+    capi.fno_layer_norm_bwd(d, x, gamma, mean, rstd, dy, dx, dg, db)
+    r = rstd.double()[:, None]
+    xh = (x.double() - mean.double()[:, None]) * r
+    gg = dy.double() * gamma.double()[:, None]
+    ref = r * (gg - gg.mean(1, keepdim=True) - xh * (gg * xh).mean(1, keepdim=True))
+    tol = r * (C + 16) * U * (gg.abs() + gg.abs().mean(1, keepdim=True)
+                              + xh.abs() * (gg * xh).abs().mean(1, keepdim=True))
+    tol = tol + HALF[dtype] * (ref.abs() + tol) + TINY[dtype]
+    assert bool(((dx.double() - ref).abs() <= tol).all())
