@@ -5,10 +5,11 @@
 //   xh = (x - mean) rstd,  y = xh gamma + beta
 //   g = dy gamma,  dx = rstd (g - mean_c(g) - xh mean_c(g xh))
 //   dgamma[c] = sum_points dy xh,  dbeta[c] = sum_points dy
-// All sums are float32.  The variance is taken about a first mean m0 in a second
-// sweep over the values, which also gives e = mean(x - m0), the rounding of m0:
-// mean = m0 + e, var = mean((x - m0)^2) - e^2, xh = ((x - m0) - e) rstd, so a
-// common offset far above the spread costs no more than the offset's own storage.
+// All sums are float32 (over many channels compensated: Sum).  The variance is taken
+// about a first mean m0 in a second sweep over the values, which also gives
+// e = mean(x - m0), the rounding of m0: mean = m0 + e, var = mean((x - m0)^2) - e^2,
+// xh = ((x - m0) - e) rstd, so a common offset far above the spread costs no more than
+// the offset's own storage.
 #include "norm_common.cuh"
 
 namespace fno {
@@ -39,6 +40,19 @@ __device__ __forceinline__ float cta_sum(float v, float *sh) {
 // any channel count: the values are read again in each sweep
 // ---------------------------------------------------------------------------
 
+// A thread's sum of many values with the rounding of every addition kept beside it and
+// made good by the next (Kahan, "Further remarks on reducing truncation errors"): off by
+// two units of 2^-24 of the sum of the values' sizes, however many they are.  (One
+// float32 chain of 4099 equal values was off by 690 units, one of 2^20 values by 1 %.)
+struct Sum {
+  float s = 0.f, lost = 0.f;
+  __device__ __forceinline__ void add(float v) {
+    const float w = v - lost, t = s + w;
+    lost = (t - s) - w;
+    s = t;
+  }
+};
+
 // thread per point (inner > 1: neighbouring threads read neighbouring points)
 template <typename T>
 __global__ void __launch_bounds__(LT)
@@ -48,17 +62,15 @@ __global__ void __launch_bounds__(LT)
   const long long stride = (long long)gridDim.x * LT;
   for (long long p = (long long)blockIdx.x * LT + threadIdx.x; p < points; p += stride) {
     const long long b = p / inner, base = b * C * inner + (p - b * inner);
-    float m0 = 0.f;
-    for (int c = 0; c < C; ++c) m0 += to_f<T>(x[base + c * inner]);
-    m0 *= inv_c;
-    float e = 0.f, q = 0.f;
+    Sum m, es, q;
+    for (int c = 0; c < C; ++c) m.add(to_f<T>(x[base + c * inner]));
+    const float m0 = m.s * inv_c;
     for (int c = 0; c < C; ++c) {
       const float d = to_f<T>(x[base + c * inner]) - m0;
-      e += d;
-      q = fmaf(d, d, q);
+      es.add(d);
+      q.add(d * d);
     }
-    e *= inv_c;
-    const float r = ln_rstd(q * inv_c, e, eps);
+    const float e = es.s * inv_c, r = ln_rstd(q.s * inv_c, e, eps);
     if (mean) {
       mean[p] = m0 + e;
       rstd[p] = r;
@@ -71,6 +83,14 @@ __global__ void __launch_bounds__(LT)
   }
 }
 
+// The values of channels c .. c + 7 of a point, all on their way before the first is
+// used; beyond the last channel that one again.
+template <typename T>
+__device__ __forceinline__ void next8(const T *p, long long hop, int c, int C, float *v) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = to_f<T>(p[(c + i < C ? c + i : C - 1) * hop]);
+}
+
 template <typename T>
 __global__ void __launch_bounds__(LT)
     k_ln_bwd_point(const T *__restrict__ x, const T *__restrict__ gamma,
@@ -80,14 +100,21 @@ __global__ void __launch_bounds__(LT)
   for (long long p = (long long)blockIdx.x * LT + threadIdx.x; p < points; p += stride) {
     const long long b = p / inner, base = b * C * inner + (p - b * inner);
     const float mu = mean[p], r = rstd[p];
-    float c1 = 0.f, c2 = 0.f;
-    for (int c = 0; c < C; ++c) {
-      const float g = to_f<T>(dy[base + c * inner]) * (gamma ? to_f<T>(gamma[c]) : 1.f);
-      c1 += g;
-      c2 = fmaf(g, (to_f<T>(x[base + c * inner]) - mu) * r, c2);
+    Sum gs, gx;
+    float v[8], w[8], ga[8];
+    for (int c = 0; c < C; c += 8) {
+      next8<T>(x + base, inner, c, C, v);
+      next8<T>(dy + base, inner, c, C, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ga[i] = gamma ? to_f<T>(gamma[c + i < C ? c + i : C - 1]) : 1.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float g = c + i < C ? w[i] * ga[i] : 0.f;
+        gs.add(g);
+        gx.add(g * ((v[i] - mu) * r));
+      }
     }
-    c1 *= inv_c;
-    c2 *= inv_c;
+    const float c1 = gs.s * inv_c, c2 = gx.s * inv_c;
     for (int c = 0; c < C; ++c) {
       const float g = to_f<T>(dy[base + c * inner]) * (gamma ? to_f<T>(gamma[c]) : 1.f);
       const float xh = (to_f<T>(x[base + c * inner]) - mu) * r;
@@ -129,18 +156,16 @@ __global__ void __launch_bounds__(LT)
   for (long long p = blockIdx.x; p < rows; p += gridDim.x) {
     const T *xr = x + p * C;
     T *yr = y + p * C;
-    float m0 = 0.f;
-    for (int c = threadIdx.x; c < C; c += LT) m0 += to_f<T>(xr[c]);
-    m0 = cta_sum(m0, sh) * inv_c;
-    float e = 0.f, q = 0.f;
+    Sum m, es, q;
+    for (int c = threadIdx.x; c < C; c += LT) m.add(to_f<T>(xr[c]));
+    const float m0 = cta_sum(m.s, sh) * inv_c;
     for (int c = threadIdx.x; c < C; c += LT) {
       const float d = to_f<T>(xr[c]) - m0;
-      e += d;
-      q = fmaf(d, d, q);
+      es.add(d);
+      q.add(d * d);
     }
-    e = cta_sum(e, sh) * inv_c;
-    q = cta_sum(q, sh);
-    const float r = ln_rstd(q * inv_c, e, eps);
+    const float e = cta_sum(es.s, sh) * inv_c;
+    const float r = ln_rstd(cta_sum(q.s, sh) * inv_c, e, eps);
     if (mean && threadIdx.x == 0) {
       mean[p] = m0 + e;
       rstd[p] = r;
@@ -160,14 +185,13 @@ __global__ void __launch_bounds__(LT)
   __shared__ float sh[LT / 32];
   for (long long p = blockIdx.x; p < rows; p += gridDim.x) {
     const float mu = mean[p], r = rstd[p];
-    float c1 = 0.f, c2 = 0.f;
+    Sum gs, gx;
     for (int c = threadIdx.x; c < C; c += LT) {
       const float g = to_f<T>(dy[p * C + c]) * (gamma ? to_f<T>(gamma[c]) : 1.f);
-      c1 += g;
-      c2 = fmaf(g, (to_f<T>(x[p * C + c]) - mu) * r, c2);
+      gs.add(g);
+      gx.add(g * ((to_f<T>(x[p * C + c]) - mu) * r));
     }
-    c1 = cta_sum(c1, sh) * inv_c;
-    c2 = cta_sum(c2, sh) * inv_c;
+    const float c1 = cta_sum(gs.s, sh) * inv_c, c2 = cta_sum(gx.s, sh) * inv_c;
     for (int c = threadIdx.x; c < C; c += LT) {
       const float g = to_f<T>(dy[p * C + c]) * (gamma ? to_f<T>(gamma[c]) : 1.f);
       const float xh = (to_f<T>(x[p * C + c]) - mu) * r;

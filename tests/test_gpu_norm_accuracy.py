@@ -1,5 +1,5 @@
 """Layer norm where its accuracy could get lost: points without spread, values far
-from one.
+from one, sums over many channels.
 
 Tolerances.  u = 2^-24 is half a float32 step; a storage rounding is off by at
 most finfo(t).eps / 2 of the value (and by half the smallest subnormal).
@@ -136,3 +136,48 @@ def test_layer_norm_backward_far_from_one(shape, dtype, spread, size, eps):
                               + xh.abs() * (gg * xh).abs().mean(1, keepdim=True))
     tol = tol + HALF[dtype] * (ref.abs() + tol) + TINY[dtype]
     assert bool(((dx.double() - ref).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("shape", [(1, 1100, 5), (1, 4099, 6), (2, 33000, 3), (2, 33000, 1),
+                                   (1, 100003, 3), (1, 100003, 1), (1, 1 << 20, 2),
+                                   (2, 1 << 20, 1)], ids=str)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_layer_norm_sums_over_many_channels(shape, dtype):
+    """Values of one sign and nearly one size, whose roundings add up in a long chain.
+
+    A thread's sum over the channels is compensated: off by 2 u and C u^2 <= u / 16 of its
+    terms' sizes, whose own products are rounded once; where threads share a row, five
+    steps of a warp's and eight of a CTA's sum follow.  That is n = 20 roundings at most,
+    whatever C is, and the tolerances are those with C terms, with n in the place of C:
+    y (2 n + 16) u (1 + |xh|) |gamma| + 4 u |y|; dx rstd (n + 16) u (|g| + mean|g| + |xh|
+    mean|g xh|); each with its rounding to storage."""
+    import torch
+    outer, C, inner = shape
+    n = 20
+    g = torch.Generator(device="cuda").manual_seed(59)
+    dt = torch_dtype(dtype)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    x = (1.1 + 0.02 * rnd(*shape)).to(dt)
+    dy = (0.1 + 0.001 * rnd(*shape)).to(dt)
+    gamma, beta = (1 + 0.02 * rnd(C)).to(dt), (0.2 * rnd(C)).to(dt)
+    d = capi.layer_norm_desc(outer, C, inner, dtype, EPS)
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    mean, rstd = (torch.empty((outer, inner), device="cuda") for _ in range(2))
+    capi.fno_layer_norm_fwd(d, x, gamma, beta, y, mean, rstd)
+    x6, ga = x.double(), gamma.double()[:, None]
+    rm = x6.mean(1, keepdim=True)
+    xh = (x6 - rm) / ((x6 - rm).square().mean(1, keepdim=True) + EPS).sqrt()
+    ry = xh * ga + beta.double()[:, None]
+    tol = (2 * n + 16) * U * (1 + xh.abs()) * ga.abs() + 4 * U * ry.abs()
+    assert bool(((y.double() - ry).abs()
+                 <= tol + HALF[dtype] * (ry.abs() + tol) + TINY[dtype]).all())
+    assert bool(((mean.double() - rm[:, 0]).abs() <= (n + 4) * U * x6.abs().mean(1)).all())
+    capi.fno_layer_norm_bwd(d, x, gamma, mean, rstd, dy, dx)
+    r = rstd.double()[:, None]
+    xh = (x6 - mean.double()[:, None]) * r
+    gg = dy.double() * ga
+    ref = r * (gg - gg.mean(1, keepdim=True) - xh * (gg * xh).mean(1, keepdim=True))
+    tol = r * (n + 16) * U * (gg.abs() + gg.abs().mean(1, keepdim=True)
+                              + xh.abs() * (gg * xh).abs().mean(1, keepdim=True))
+    assert bool(((dx.double() - ref).abs()
+                 <= tol + HALF[dtype] * (ref.abs() + tol) + TINY[dtype]).all())
