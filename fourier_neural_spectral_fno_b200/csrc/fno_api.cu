@@ -452,8 +452,11 @@ NetWs net_ws(const fno_net_desc *d, const Geom &g, int op) {
     const size_t lift = (size_t)d->width * (d->in_channels + 1);
     if (lift > p) p = lift;
     size_t bytes = sizeof(float) * kPartialCTAs * p;
-    if ((d->flags & FNO_LAYER_NORM) && ln_partial_bytes(d->width) > bytes)
-      bytes = ln_partial_bytes(d->width);
+    if (d->flags & FNO_LAYER_NORM) {
+      const size_t ln =
+          ln_partial_bytes(NormShape{g.B, g.N, d->width, FNO_NET_NORM_EPS}, d->dtype);
+      if (ln > bytes) bytes = ln;
+    }
     off += al(bytes);
   }
   w.total = off;
@@ -1118,7 +1121,7 @@ size_t fno_layer_norm_workspace_size(const fno_norm_desc *desc) {
   NormShape s;
   if (check_norm(desc, &s)) return 0;
   g_err[0] = 0;
-  return al(ln_partial_bytes(s.C));
+  return al(ln_partial_bytes(s, desc->dtype));
 }
 
 int fno_layer_norm_fwd(const fno_norm_desc *desc, const void *x, const void *gamma,
@@ -1158,7 +1161,7 @@ int fno_layer_norm_bwd(const fno_norm_desc *desc, const void *x, const void *gam
   OPTIONAL_PTR(dgamma, "dgamma");
   OPTIONAL_PTR(dbeta, "dbeta");
   if (dgamma || dbeta) {
-    const size_t need = al(ln_partial_bytes(s.C));
+    const size_t need = al(ln_partial_bytes(s, desc->dtype));
     if (ws_bytes < need)
       return fail(FNO_ERR_WORKSPACE, "workspace %zu B < %zu B", ws_bytes, need);
     REQUIRE_PTR(ws, "ws");

@@ -294,12 +294,12 @@ struct NormShape {
   float eps;
 };
 constexpr int kLnParts = 592;   // most CTAs that write partial parameter gradients
-size_t ln_partial_bytes(int C);
+size_t ln_partial_bytes(const NormShape &s, int dtype);
 // gamma, beta may be NULL (1, 0); mean, rstd [outer][inner] both or neither; y may be x
 cudaError_t launch_ln_fwd(const Launch &L, const NormShape &s, int dtype, const void *x,
                           const void *gamma, const void *beta, void *y, float *mean,
                           float *rstd);
-// dgamma, dbeta may be NULL; dx may be dy; partial: ln_partial_bytes(C)
+// dgamma, dbeta may be NULL; dx may be dy; partial: ln_partial_bytes
 cudaError_t launch_ln_bwd(const Launch &L, const NormShape &s, int dtype, const void *x,
                           const void *gamma, const float *mean, const float *rstd, const void *dy,
                           void *dx, float *dgamma, float *dbeta, float *partial);

@@ -222,6 +222,12 @@ unsigned capped(long long want, long long cap) {
   return (unsigned)(want < 1 ? 1 : want < cap ? want : cap);
 }
 
+// slices of the points, each a partial row
+int dparam_row_slices(long long rows) { return (int)capped((rows + 15) / 16, kLnParts); }
+int dparam_point_slices(long long points) {
+  return (int)capped((points + 4 * LT - 1) / (4 * LT), kLnParts);
+}
+
 // dgamma and dbeta of the kernels' partial rows [nparts][C][2].  A CTA takes COLS
 // neighbouring values, neighbouring threads neighbouring values of a row and the
 // CTA's 1024 threads as many rows as they reach; their sums meet in a fixed order.
@@ -267,7 +273,20 @@ cudaError_t reduce_params(const Launch &L, const float *partial, int nparts, int
 
 }  // namespace
 
-size_t ln_partial_bytes(int C) { return sizeof(float) * 2 * (size_t)C * kLnParts; }
+// The partial rows that no kernel exceeds for this shape on any device: a row is the work
+// of one CTA, and no CTA of the grid kernels has fewer than 32 points of a sample (the
+// pipelines and the odd grids) or of all (the register kernels).  A larger outer never
+// needs fewer rows, whichever kernels it goes to, so that a workspace serves every
+// smaller batch.
+size_t ln_partial_bytes(const NormShape &s, int dtype) {
+  const long long points = s.outer * s.inner;
+  long long rows;
+  if (ln_rows_supported(s, dtype, true)) rows = ln_rows_parts(s, dtype);
+  else if (s.inner == 1) rows = dparam_row_slices(points);
+  else if (s.C > kGridBwdChannels) rows = dparam_point_slices(points);
+  else rows = capped(s.outer * ((s.inner + 31) / 32), kLnParts);
+  return sizeof(float) * 2 * (size_t)s.C * (size_t)rows;
+}
 
 cudaError_t launch_ln_fwd(const Launch &L, const NormShape &s, int dtype, const void *x,
                           const void *gamma, const void *beta, void *y, float *mean,
@@ -330,12 +349,12 @@ cudaError_t launch_ln_bwd(const Launch &L, const NormShape &s, int dtype, const 
     int slices;
     launch_begin(L);
     if (s.inner == 1) {
-      slices = (int)capped((points + 15) / 16, kLnParts);
+      slices = dparam_row_slices(points);
       const dim3 grid((s.C + LT - 1) / LT, slices);
       FNO_DISPATCH_T(dtype, k_ln_dparam_row<T><<<grid, LT, 0, L.stream>>>(
                                 (const T *)x, mean, rstd, (const T *)dy, partial, points, s.C));
     } else {
-      slices = (int)capped((points + 4 * LT - 1) / (4 * LT), kLnParts);
+      slices = dparam_point_slices(points);
       const dim3 grid(s.C, slices);
       FNO_DISPATCH_T(dtype, k_ln_dparam_point<T><<<grid, LT, 0, L.stream>>>(
                                 (const T *)x, mean, rstd, (const T *)dy, partial, points, s.C,

@@ -191,6 +191,7 @@ __device__ __forceinline__ float ln_rstd(float q_mean, float e, float eps) {
 
 // ---- per-layout kernels -----------------------------------------------------
 // grid layout (inner > 1), values held in registers (norm_grid.cu)
+constexpr int kGridBwdChannels = 256;   // most channels of its backward
 bool ln_grid_supported(const NormShape &s, int dtype, bool bwd);
 cudaError_t launch_ln_grid_fwd(const Launch &L, const NormShape &s, int dtype, const void *x,
                                const void *gamma, const void *beta, void *y, float *mean,
@@ -211,6 +212,7 @@ cudaError_t launch_ln_odd(const Launch &L, const NormShape &s, int dtype, const 
 
 // rows (inner == 1), values held in registers (norm_rows.cu); outputs as above
 bool ln_rows_supported(const NormShape &s, int dtype, bool bwd);
+int ln_rows_parts(const NormShape &s, int dtype);   // most partial rows, on any device
 cudaError_t launch_ln_rows_fwd(const Launch &L, const NormShape &s, int dtype, const void *x,
                                const void *gamma, const void *beta, void *y, float *mean,
                                float *rstd);

@@ -370,7 +370,9 @@ cudaError_t bwd_t(const Launch &L, const NormShape &s, const void *x, const void
 // 31 bits
 bool ln_grid_supported(const NormShape &s, int dtype, bool bwd) {
   if (s.inner == 1 || s.outer * s.inner > 32LL * 0x7fffffffLL) return false;
-  if (bwd) return s.C <= 16 * 16;   // four lane groups of 4, or single elements of 16
+  // 16 warps of four lane groups of 4 channels, or of single elements of 16
+  static_assert(kGridBwdChannels == 16 * 16, "channels of the widest backward");
+  if (bwd) return s.C <= kGridBwdChannels;
   if (vec_ok(s)) return s.C <= (dtype == DT_F32 ? 4 : 2) * 16 * 16;
   return s.C <= 32 * 16;
 }

@@ -461,6 +461,12 @@ cudaError_t bwd_t(const Launch &L, const NormShape &s, int tpr, const void *x, c
   return cudaGetLastError();
 }
 
+// the backward's grid under the cap of every device
+template <typename T> int most_parts(const NormShape &s) {
+  const int tpr = pick_tpr(row_pieces<T>(s), most<T, true>(s));
+  return (int)row_grid(s.outer, row_threads(tpr) / tpr, Rows<T>::V, s.C % Rows<T>::V != 0, kLnParts);
+}
+
 template <typename T> bool fits(const NormShape &s, bool bwd) {
   return pick_tpr(row_pieces<T>(s), bwd ? most<T, true>(s) : most<T, false>(s)) != 0;
 }
@@ -470,6 +476,10 @@ template <typename T> bool fits(const NormShape &s, bool bwd) {
 bool ln_rows_supported(const NormShape &s, int dtype, bool bwd) {
   if (s.inner != 1 || s.outer > 0x7fffffffLL) return false;
   return dtype == DT_F32 ? fits<float>(s, bwd) : fits<__half>(s, bwd);
+}
+
+int ln_rows_parts(const NormShape &s, int dtype) {
+  return dtype == DT_F32 ? most_parts<float>(s) : most_parts<__half>(s);
 }
 
 cudaError_t launch_ln_rows_fwd(const Launch &L, const NormShape &s, int dtype, const void *x,

@@ -396,8 +396,10 @@ typedef struct fno_norm_desc {
   float eps;     /* > 0 */
 } fno_norm_desc;
 
-/* Workspace bytes of fno_layer_norm_bwd (the forward needs none); 0 for an
- * invalid descriptor. */
+/* Workspace bytes of fno_layer_norm_bwd (the forward needs none): 8 bytes per
+ * channel for each of up to 592 groups of points.  A larger outer never needs
+ * less, so the largest batch's workspace serves the others.  0 for an invalid
+ * descriptor. */
 size_t fno_layer_norm_workspace_size(const fno_norm_desc *desc);
 
 /* y [outer][channels][inner] (storage dtype; may be x itself).  gamma, beta
