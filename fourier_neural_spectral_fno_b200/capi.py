@@ -50,7 +50,7 @@ EXPORTED = (
     "fno_backward_ready", "fno_spectral_conv_fwd_cp", "fno_block_fwd_cp", "fno_set_wait_limit",
     "fno_spectral_conv_bwd_cp", "fno_block_bwd_cp", "fno_layer_norm_workspace_size",
     "fno_layer_norm_fwd", "fno_layer_norm_bwd", "fno_grad_norm_workspace_size", "fno_grad_norm",
-    "fno_clip_grads", "fno_adam_step_clipped",
+    "fno_clip_grads", "fno_adam_step_clipped", "fno_adam_step_skipping",
 )
 
 FNO_MAX_CP_RANK = 32
@@ -153,6 +153,8 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
                               ctypes.c_float, vp]),
         "fno_adam_step_clipped": (i, [ctypes.c_int64, vp, vp, vp, vp, vp, i, i, f, f, f, f, f, f,
                                       vp, i, vp]),
+        "fno_adam_step_skipping": (i, [ctypes.c_int64, vp, vp, vp, vp, vp, i, i, f, f, f, f, f,
+                                       f, vp, vp, vp]),
         "fno_layer_norm_workspace_size": (sz, [ld]),
         "fno_layer_norm_fwd": (i, [ld, vp, vp, vp, vp, vp, vp, vp]),
         "fno_layer_norm_bwd": (i, [ld, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
@@ -471,13 +473,29 @@ def fno_adam_step(theta, m, v, grad, param_out, step: int, lr: float, beta1: flo
                                 _stream(stream)))
 
 
+class SkippedSteps:
+    """The count of the steps that an optimiser skipped, on the device; handed to
+    :func:`fno_adam_step_clipped` in every step."""
+
+    def __init__(self, device):
+        import torch
+        self.state = torch.zeros(4, dtype=torch.int32, device=device)
+
+    def count(self) -> int:
+        """Steps skipped so far (waits for the device)."""
+        return int(self.state[0])
+
+
 def fno_adam_step_clipped(theta, m, v, grad, param_out, step: int, lr: float, norm,
                           beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
                           weight_decay: float = 0.0, grad_scale: float = 1.0,
-                          skip_nonfinite: bool = False, stream=None):
+                          skip_nonfinite=False, stream=None):
     """:func:`fno_adam_step` with the gradient also multiplied by ``norm[1]``
     (float32 device tensor of two, from :func:`fno_grad_norm`).
-    ``skip_nonfinite``: a norm that is not finite leaves the state as it is."""
+    ``skip_nonfinite``: a norm that is not finite leaves the state as it is.  True:
+    ``step`` is the bias correction's t as given; a :class:`SkippedSteps`: the steps
+    that it has counted are taken off ``step``, and this one is counted if skipped
+    (``fno_adam_step_skipping``)."""
     out_code = _dtype_code_of(param_out) if param_out is not None else FNO_F32
     n, dev, f32 = theta.numel(), _device_index(theta, "theta"), _torch_dtypes()[0]
     for t, name in ((theta, "theta"), (m, "m"), (v, "v"), (grad, "grad")):
@@ -485,9 +503,14 @@ def fno_adam_step_clipped(theta, m, v, grad, param_out, step: int, lr: float, no
     if param_out is not None:
         _check_tensor(param_out, "param_out", param_out.dtype, n, dev)
     _check_tensor(norm, "norm", f32, 2, dev)
-    _run(load().fno_adam_step_clipped, dev, stream, n, _ptr(theta), _ptr(m), _ptr(v), _ptr(grad),
+    fn, skip = load().fno_adam_step_clipped, 1 if skip_nonfinite else 0
+    if isinstance(skip_nonfinite, SkippedSteps):
+        _check_tensor(skip_nonfinite.state, "skip_nonfinite.state",
+                      skip_nonfinite.state.dtype, 4, dev)
+        fn, skip = load().fno_adam_step_skipping, _ptr(skip_nonfinite.state)
+    _run(fn, dev, stream, n, _ptr(theta), _ptr(m), _ptr(v), _ptr(grad),
          _ptr(param_out), out_code, int(step), float(lr), float(beta1), float(beta2), float(eps),
-         float(weight_decay), float(grad_scale), _ptr(norm), 1 if skip_nonfinite else 0)
+         float(weight_decay), float(grad_scale), _ptr(norm), skip)
 
 
 # --------------------------------------------------------------------------

@@ -1037,7 +1037,8 @@ int fno_mse(int64_t n, int dtype, const void *u, const void *target, float *loss
 static int adam_step(int64_t n, float *theta, float *m, float *v, const float *grad,
                      void *param_out, int out_dtype, int step, float lr, float beta1,
                      float beta2, float eps, float weight_decay, float grad_scale,
-                     const float *norm, bool skip_nonfinite, fno_stream_t stream) {
+                     const float *norm, bool skip_nonfinite, int32_t *skipped,
+                     fno_stream_t stream) {
   if (n < 1) return fail(FNO_ERR_INVALID_ARG, "n %lld < 1", (long long)n);
   REQUIRE_PTR(theta, "theta");
   OPTIONAL_PTR(param_out, "param_out");
@@ -1070,8 +1071,11 @@ static int adam_step(int64_t n, float *theta, float *m, float *v, const float *g
     return fail(FNO_ERR_INVALID_ARG, "neither grad nor param_out given: nothing to do");
   }
   Launch L = make_launch(stream);
+  if (skipped)
+    FNO_TRY(launch_adam_skips(L, step, beta1, beta2, c, norm, skipped), "counting skipped steps");
   FNO_TRY(launch_adam(L, n, theta, grad ? m : nullptr, grad ? v : nullptr, grad, param_out,
-                      out_dtype, c, norm, skip_nonfinite),
+                      out_dtype, c, norm, skip_nonfinite,
+                      skipped ? reinterpret_cast<const float *>(skipped + 1) : nullptr),
           "adam");
   g_err[0] = 0;
   return FNO_OK;
@@ -1081,7 +1085,7 @@ int fno_adam_step(int64_t n, float *theta, float *m, float *v, const float *grad
                   void *param_out, int out_dtype, int step, float lr, float beta1, float beta2,
                   float eps, float weight_decay, float grad_scale, fno_stream_t stream) {
   return adam_step(n, theta, m, v, grad, param_out, out_dtype, step, lr, beta1, beta2, eps,
-                   weight_decay, grad_scale, nullptr, false, stream);
+                   weight_decay, grad_scale, nullptr, false, nullptr, stream);
 }
 
 int fno_adam_step_clipped(int64_t n, float *theta, float *m, float *v, const float *grad,
@@ -1092,7 +1096,19 @@ int fno_adam_step_clipped(int64_t n, float *theta, float *m, float *v, const flo
   if (!norm) return fail(FNO_ERR_INVALID_ARG, "norm is NULL");
   if ((uintptr_t)norm & 3) return fail(FNO_ERR_INVALID_ARG, "norm is not 4-byte aligned");
   return adam_step(n, theta, m, v, grad, param_out, out_dtype, step, lr, beta1, beta2, eps,
-                   weight_decay, grad_scale, norm, skip_nonfinite != 0, stream);
+                   weight_decay, grad_scale, norm, skip_nonfinite != 0, nullptr, stream);
+}
+
+int fno_adam_step_skipping(int64_t n, float *theta, float *m, float *v, const float *grad,
+                           void *param_out, int out_dtype, int step, float lr, float beta1,
+                           float beta2, float eps, float weight_decay, float grad_scale,
+                           const float *norm, int32_t *skipped, fno_stream_t stream) {
+  REQUIRE_PTR(grad, "grad");
+  if (!norm) return fail(FNO_ERR_INVALID_ARG, "norm is NULL");
+  if ((uintptr_t)norm & 3) return fail(FNO_ERR_INVALID_ARG, "norm is not 4-byte aligned");
+  REQUIRE_PTR(skipped, "skipped");
+  return adam_step(n, theta, m, v, grad, param_out, out_dtype, step, lr, beta1, beta2, eps,
+                   weight_decay, grad_scale, norm, true, skipped, stream);
 }
 
 // ---------------------------------------------------------------------------

@@ -281,10 +281,16 @@ struct AdamCoef {
 };
 // clip (optional, device): (norm, factor) as launch_grad_norm writes them; the
 // gradient is multiplied by the factor, and with skip_nonfinite a norm that is
-// not finite leaves theta, m and v as they are (out is still written)
+// not finite leaves theta, m and v as they are (out is still written).  bias
+// (optional, device): 1 / (1 - beta1^t), 1 / (1 - beta2^t) in place of c's
 cudaError_t launch_adam(const Launch &L, long long n, float *theta, float *m, float *v,
                         const float *g, void *out, int out_dtype, const AdamCoef &c,
-                        const float *clip = nullptr, bool skip_nonfinite = false);
+                        const float *clip = nullptr, bool skip_nonfinite = false,
+                        const float *bias = nullptr);
+// In front of it: skipped[0] counts the steps whose norm is not finite, skipped[1]
+// and [2] receive launch_adam's bias for t = step - (steps skipped before)
+cudaError_t launch_adam_skips(const Launch &L, int step, float beta1, float beta2,
+                              const AdamCoef &c, const float *norm, int *skipped);
 
 // ---- layer normalisation (norm.cu) ----------------------------------------
 // over the C channels of x [outer][C][inner]

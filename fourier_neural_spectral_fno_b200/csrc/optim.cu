@@ -52,6 +52,26 @@ template <> __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16 
   *reinterpret_cast<uint2 *>(p) = u;
 }
 
+__device__ __forceinline__ bool finite_norm(const float *norm) {
+  return norm[0] <= 3.402823466e38f;   // a norm is not negative; a NaN is not finite
+}
+
+// One thread, in front of the step: a launch of its own, so that the count changes
+// after every CTA of the step before has read what belongs to it.  Without a skipped
+// step the bias is the host's, bit for bit.
+__global__ void k_adam_skips(int step, double beta1, double beta2, float inv_bc1, float inv_bc2,
+                             const float *norm, int *skipped) {
+  const int n = skipped[0];
+  if (n > 0) {
+    const double t = step > n ? step - n : 1;
+    inv_bc1 = (float)(1.0 / (1.0 - pow(beta1, t)));
+    inv_bc2 = (float)(1.0 / (1.0 - pow(beta2, t)));
+  }
+  skipped[1] = __float_as_int(inv_bc1);
+  skipped[2] = __float_as_int(inv_bc2);
+  if (!finite_norm(norm)) skipped[0] = n + 1;
+}
+
 // n4 groups of four through 16-byte accesses, then the n - 4 n4 tail.  With
 // `clip` (norm, factor) the gradient scale takes the factor; a step skipped for
 // a norm that is not finite is the copy alone.
@@ -59,10 +79,14 @@ template <typename T>
 __global__ void __launch_bounds__(AT)
     k_adam(long long n, long long n4, float *__restrict__ theta, float *__restrict__ m,
            float *__restrict__ v, const float *__restrict__ g, T *__restrict__ out, AdamCoef c,
-           const float *__restrict__ clip, bool skip_nonfinite) {
+           const float *__restrict__ clip, bool skip_nonfinite, const float *__restrict__ bias) {
   if (clip) {
-    if (skip_nonfinite && !(clip[0] <= 3.402823466e38f)) g = nullptr;
+    if (skip_nonfinite && !finite_norm(clip)) g = nullptr;
     c.grad_scale *= clip[1];
+  }
+  if (bias) {
+    c.inv_bc1 = bias[0];
+    c.inv_bc2 = bias[1];
   }
   const long long stride = (long long)gridDim.x * AT;
   for (long long i = (long long)blockIdx.x * AT + threadIdx.x; i < n4; i += stride) {
@@ -100,7 +124,7 @@ bool al8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7) == 0; }
 template <typename T>
 cudaError_t launch_adam_t(const Launch &L, long long n, float *theta, float *m, float *v,
                           const float *g, void *out, const AdamCoef &c, const float *clip,
-                          bool skip_nonfinite) {
+                          bool skip_nonfinite, const float *bias) {
   // 16-byte groups need 16-byte aligned float arrays and an aligned 4-element copy
   const bool vec = al16(theta) && (!g || (al16(m) && al16(v) && al16(g))) &&
                    (!out || (sizeof(T) == 4 ? al16(out) : al8(out)));
@@ -112,7 +136,7 @@ cudaError_t launch_adam_t(const Launch &L, long long n, float *theta, float *m, 
   if (blocks < 1) blocks = 1;
   k_adam<T><<<(unsigned)blocks, AT, 0, L.stream>>>(n, n4, theta, m, v, g,
                                                    reinterpret_cast<T *>(out), c, clip,
-                                                   skip_nonfinite);
+                                                   skip_nonfinite, bias);
   return cudaGetLastError();
 }
 
@@ -120,16 +144,26 @@ cudaError_t launch_adam_t(const Launch &L, long long n, float *theta, float *m, 
 
 cudaError_t launch_adam(const Launch &L, long long n, float *theta, float *m, float *v,
                         const float *g, void *out, int out_dtype, const AdamCoef &c,
-                        const float *clip, bool skip_nonfinite) {
+                        const float *clip, bool skip_nonfinite, const float *bias) {
   launch_begin(L);
   cudaError_t err;
   if (out_dtype == DT_F16)
-    err = launch_adam_t<__half>(L, n, theta, m, v, g, out, c, clip, skip_nonfinite);
+    err = launch_adam_t<__half>(L, n, theta, m, v, g, out, c, clip, skip_nonfinite, bias);
   else if (out_dtype == DT_BF16)
-    err = launch_adam_t<__nv_bfloat16>(L, n, theta, m, v, g, out, c, clip, skip_nonfinite);
+    err = launch_adam_t<__nv_bfloat16>(L, n, theta, m, v, g, out, c, clip, skip_nonfinite, bias);
   else
-    err = launch_adam_t<float>(L, n, theta, m, v, g, out, c, clip, skip_nonfinite);
+    err = launch_adam_t<float>(L, n, theta, m, v, g, out, c, clip, skip_nonfinite, bias);
   launch_end(L, g ? "adam" : "cast_params");
+  return err;
+}
+
+cudaError_t launch_adam_skips(const Launch &L, int step, float beta1, float beta2,
+                              const AdamCoef &c, const float *norm, int *skipped) {
+  launch_begin(L);
+  k_adam_skips<<<1, 1, 0, L.stream>>>(step, (double)beta1, (double)beta2, c.inv_bc1, c.inv_bc2,
+                                      norm, skipped);
+  const cudaError_t err = cudaGetLastError();
+  launch_end(L, "adam_skips");
   return err;
 }
 

@@ -32,7 +32,7 @@ from typing import Dict, List, Optional, Sequence, Tuple
 import numpy as np
 
 from . import capi
-from .capi import FNO_LAYER_NORM
+from .capi import FNO_LAYER_NORM, SkippedSteps
 
 STORAGE_DTYPES = ("f32", "f16", "bf16")
 ALIGN = 8   # elements per slot boundary: 16 bytes in every storage dtype
@@ -187,8 +187,10 @@ class Trainer:
     ``ln_g``, ``ln_b``, one [width] per layer).
     ``max_grad_norm``: clip the (averaged) gradient to this global norm.
     ``skip_nonfinite``: a step whose gradient norm is not finite (an overflow of
-    half precision) changes no weight and no moment.  With either, ``grad_norm``
-    holds the last step's norm and clipping factor (float32 device tensor).
+    half precision) changes no weight and no moment and does not count in Adam's
+    bias correction (``step_count`` and the schedule go on; :meth:`skipped_steps`).
+    With either, ``grad_norm`` holds the last step's norm and clipping factor
+    (float32 device tensor).
     """
 
     def __init__(self, grid: Sequence[int], modes: Sequence[int], in_channels: int, width: int,
@@ -220,6 +222,9 @@ class Trainer:
         self.max_grad_norm, self.skip_nonfinite = max_grad_norm, skip_nonfinite
         self.grad_norm = None     # (norm, factor) of the last step, where it is taken
         self._grad_list = self._norm_ws = None
+        # the steps skipped, counted on the device, and those already taken off Adam's t
+        self._skips = SkippedSteps(self.device) if skip_nonfinite else None
+        self._skipped_before = 0
         self.step_count = 0
         self.dtype: Optional[str] = None
         self.weights = None
@@ -260,6 +265,10 @@ class Trainer:
             self.weights, self.dtype = w, dtype
         return self.weights
 
+    def skipped_steps(self) -> int:
+        """Steps skipped so far (waits for the device)."""
+        return self._skipped_before + (self._skips.count() if self._skips else 0)
+
     def params(self) -> Dict[str, object]:
         """The float32 master weights as a NumPy float64 dict (R complex)."""
         return self.layout.unpack(self.master)
@@ -271,7 +280,8 @@ class Trainer:
                 "v": self.v.detach().cpu().clone(), "step": self.step_count,
                 "phases": list(self.schedule.phases), "lr": self.lr, "betas": tuple(self.betas),
                 "eps": self.eps, "weight_decay": self.weight_decay, "slots": self.layout.total,
-                "max_grad_norm": self.max_grad_norm, "skip_nonfinite": self.skip_nonfinite}
+                "max_grad_norm": self.max_grad_norm, "skip_nonfinite": self.skip_nonfinite,
+                "skipped": self.skipped_steps()}
 
     def load_state_dict(self, state: Dict[str, object]) -> None:
         """Resume from :meth:`state_dict` (same network shape)."""
@@ -286,6 +296,9 @@ class Trainer:
         self.eps, self.weight_decay = float(state["eps"]), float(state["weight_decay"])
         self.max_grad_norm = state.get("max_grad_norm", self.max_grad_norm)   # absent from
         self.skip_nonfinite = bool(state.get("skip_nonfinite", self.skip_nonfinite))  # older ones
+        self._skipped_before = int(state.get("skipped", 0))
+        if self._skips is not None:
+            self._skips.state.zero_()
         self.dtype, self.weights = None, None     # the next step copies the master afresh
 
     def _allreduce_buckets(self) -> None:
@@ -315,6 +328,16 @@ class Trainer:
         limit = float("inf") if self.max_grad_norm is None else self.max_grad_norm
         capi.fno_grad_norm(self._grad_list, limit, self.grad_norm, grad_scale=scale,
                            ws=self._norm_ws)
+
+    def _skip_state(self):
+        """The step's ``skip_nonfinite``: the count on the device, or False (the count
+        from before the flag was taken back then goes to the host's)."""
+        if not self.skip_nonfinite:
+            self._skipped_before, self._skips = self.skipped_steps(), None
+            return False
+        if self._skips is None:
+            self._skips = SkippedSteps(self.device)
+        return self._skips
 
     # ------------------------------------------------------------------- step
     def step(self, a, target):
@@ -358,15 +381,15 @@ class Trainer:
         nxt = self.schedule.dtype_at(self.step_count)
         out = w if nxt == dt else torch.empty(self.layout.total, dtype=torch_dtype(nxt),
                                               device=self.device)
-        if self.max_grad_norm is not None or self.skip_nonfinite:
+        skip = self._skip_state()
+        t = self.step_count - self._skipped_before   # of which the skips are taken off on the device
+        if self.max_grad_norm is not None or skip:
             self._take_norm(scale)
-            capi.fno_adam_step_clipped(self.master, self.m, self.v, self.grad, out,
-                                       self.step_count, self.lr, self.grad_norm, self.betas[0],
-                                       self.betas[1], self.eps, self.weight_decay, scale,
-                                       self.skip_nonfinite)
+            capi.fno_adam_step_clipped(self.master, self.m, self.v, self.grad, out, t, self.lr,
+                                       self.grad_norm, self.betas[0], self.betas[1], self.eps,
+                                       self.weight_decay, scale, skip)
         else:
-            capi.fno_adam_step(self.master, self.m, self.v, self.grad, out, self.step_count,
-                               self.lr, self.betas[0], self.betas[1], self.eps,
-                               self.weight_decay, scale)
+            capi.fno_adam_step(self.master, self.m, self.v, self.grad, out, t, self.lr,
+                               self.betas[0], self.betas[1], self.eps, self.weight_decay, scale)
         self.weights, self.dtype = out, nxt
         return b["loss"].clone()

@@ -451,11 +451,24 @@ int fno_clip_grads(int n_tensors, const void *const *grads, void *const *out,
  * fno_grad_norm on the same stream), so a clipped step writes no clipped
  * gradients: g = grad * (grad_scale * norm[1]).  grad is required.
  * skip_nonfinite != 0: where norm[0] is not finite (an overflow of half
- * precision), theta, m and v stay as they are and param_out is theta's copy. */
+ * precision), theta, m and v stay as they are and param_out is theta's copy.
+ * step is the t of the bias correction as given: a caller that goes on counting
+ * over skipped steps takes fno_adam_step_skipping. */
 int fno_adam_step_clipped(int64_t n, float *theta, float *m, float *v, const float *grad,
                           void *param_out, int out_dtype, int step, float lr, float beta1,
                           float beta2, float eps, float weight_decay, float grad_scale,
                           const float *norm, int skip_nonfinite, fno_stream_t stream);
+
+/* fno_adam_step_clipped with skip_nonfinite for a caller that counts every call
+ * and does not look at the norm: the skipped steps are counted on the device,
+ * and t = step - (steps skipped before), so that a skipped step leaves no trace
+ * in the next one's bias correction.  skipped: device, four int32, zeroed before
+ * the first call; [0] is the number of steps skipped so far, [1..3] are the
+ * library's.  One step's calls and the next's follow one another on a stream. */
+int fno_adam_step_skipping(int64_t n, float *theta, float *m, float *v, const float *grad,
+                           void *param_out, int out_dtype, int step, float lr, float beta1,
+                           float beta2, float eps, float weight_decay, float grad_scale,
+                           const float *norm, int32_t *skipped, fno_stream_t stream);
 
 #ifdef __cplusplus
 }
