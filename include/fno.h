@@ -431,9 +431,12 @@ int fno_layer_norm_bwd(const fno_norm_desc *desc, const void *x, const void *gam
  * looked at), all in one dtype; both arrays are read before the call returns.
  * Pointers need only their elements' alignment (16-byte aligned tensors are
  * read fastest).  norm: device, two float32.  max_norm >= 0, INFINITY for the
- * norm alone.  A norm of infinity gives the factor 0, a NaN gives NaN.  The
- * sums are float64 in a fixed order, so squares beyond float32's range are
- * held and equal calls give equal bits.  At most 2^40 elements in all. */
+ * norm alone.  A norm of infinity gives the factor 0 (1 where max_norm is
+ * INFINITY too: nothing is clipped), a NaN gives NaN.  The sums are float64 in
+ * a fixed order, so squares beyond float32's range are held and equal calls
+ * give equal bits; a norm beyond that range reads as infinity in norm[0], while
+ * the factor is still max_norm over the norm itself.  At most 2^40 elements in
+ * all. */
 size_t fno_grad_norm_workspace_size(int n_tensors);
 int fno_grad_norm(int n_tensors, const void *const *grads, const int64_t *sizes, int dtype,
                   float grad_scale, float max_norm, float *norm, void *ws, size_t ws_bytes,
