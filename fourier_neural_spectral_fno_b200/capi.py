@@ -242,11 +242,20 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream
 
 
-def _workspace(nbytes: int, device, ws):
+def _workspace(nbytes: int, device, ws, stream=None):
+    """The caller's workspace, or a fresh one.  With a stream given it comes out of that
+    stream's memory: the current one's could still be in use by work queued there, and
+    would be handed out again before the given stream is done with it."""
     import torch
     if ws is not None:
         return ws, ws.numel() * ws.element_size()
-    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device), max(nbytes, 256)
+    nb = max(nbytes, 256)
+    if stream is None or torch.device(device).type != "cuda":
+        return torch.empty(nb, dtype=torch.uint8, device=device), nb
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nb, dtype=torch.uint8, device=device), nb
 
 
 def fno_workspace_size(desc: BlockDesc, op: int) -> int:
@@ -271,14 +280,14 @@ def fno_net_saves_size(desc: NetDesc) -> int:
 
 
 def fno_spectral_conv_fwd(desc, x, R, y, xhat_save=None, ws=None, stream=None):
-    ws, nb = _workspace(fno_workspace_size(desc, FNO_OP_SPECTRAL_FWD), x.device, ws)
+    ws, nb = _workspace(fno_workspace_size(desc, FNO_OP_SPECTRAL_FWD), x.device, ws, stream)
     _check(load().fno_spectral_conv_fwd(ctypes.byref(desc), _ptr(x), _ptr(R), _ptr(y),
                                         _ptr(xhat_save), _ptr(ws), nb, _stream(stream)))
     return y
 
 
 def fno_spectral_conv_bwd(desc, x, xhat_save, R, dy, dx, dR, ws=None, stream=None):
-    ws, nb = _workspace(fno_workspace_size(desc, FNO_OP_SPECTRAL_BWD), x.device, ws)
+    ws, nb = _workspace(fno_workspace_size(desc, FNO_OP_SPECTRAL_BWD), x.device, ws, stream)
     _check(load().fno_spectral_conv_bwd(ctypes.byref(desc), _ptr(x), _ptr(xhat_save), _ptr(R),
                                         _ptr(dy), _ptr(dx), _ptr(dR), _ptr(ws), nb,
                                         _stream(stream)))
@@ -286,7 +295,7 @@ def fno_spectral_conv_bwd(desc, x, xhat_save, R, dy, dx, dR, ws=None, stream=Non
 
 
 def fno_block_fwd(desc, x, R, W, b, y, pre_save=None, xhat_save=None, ws=None, stream=None):
-    ws, nb = _workspace(fno_workspace_size(desc, FNO_OP_BLOCK_FWD), x.device, ws)
+    ws, nb = _workspace(fno_workspace_size(desc, FNO_OP_BLOCK_FWD), x.device, ws, stream)
     _check(load().fno_block_fwd(ctypes.byref(desc), _ptr(x), _ptr(R), _ptr(W), _ptr(b), _ptr(y),
                                 _ptr(pre_save), _ptr(xhat_save), _ptr(ws), nb, _stream(stream)))
     return y
@@ -295,7 +304,7 @@ def fno_block_fwd(desc, x, R, W, b, y, pre_save=None, xhat_save=None, ws=None, s
 def fno_spectral_conv_fwd_cp(desc, rank, x, lam, A, B, C, y, xhat_save=None, ws=None,
                              stream=None):
     """Spectral forward with CP-factorised weights (factors [..][rank][2])."""
-    ws, nb = _workspace(fno_workspace_size(desc, FNO_OP_SPECTRAL_FWD), x.device, ws)
+    ws, nb = _workspace(fno_workspace_size(desc, FNO_OP_SPECTRAL_FWD), x.device, ws, stream)
     _check(load().fno_spectral_conv_fwd_cp(ctypes.byref(desc), int(rank), _ptr(x), _ptr(lam),
                                            _ptr(A), _ptr(B), _ptr(C), _ptr(y), _ptr(xhat_save),
                                            _ptr(ws), nb, _stream(stream)))
@@ -305,7 +314,7 @@ def fno_spectral_conv_fwd_cp(desc, rank, x, lam, A, B, C, y, xhat_save=None, ws=
 def fno_block_fwd_cp(desc, rank, x, lam, A, B, C, W, b, y, pre_save=None, xhat_save=None,
                      ws=None, stream=None):
     """Block forward with CP-factorised weights (factors [..][rank][2])."""
-    ws, nb = _workspace(fno_workspace_size(desc, FNO_OP_BLOCK_FWD), x.device, ws)
+    ws, nb = _workspace(fno_workspace_size(desc, FNO_OP_BLOCK_FWD), x.device, ws, stream)
     _check(load().fno_block_fwd_cp(ctypes.byref(desc), int(rank), _ptr(x), _ptr(lam), _ptr(A),
                                    _ptr(B), _ptr(C), _ptr(W), _ptr(b), _ptr(y), _ptr(pre_save),
                                    _ptr(xhat_save), _ptr(ws), nb, _stream(stream)))
@@ -315,7 +324,7 @@ def fno_block_fwd_cp(desc, rank, x, lam, A, B, C, W, b, y, pre_save=None, xhat_s
 def fno_spectral_conv_bwd_cp(desc, rank, x, lam, A, B, C, xhat_save, dy, dx, dlam, dA, dB, dC,
                              ws=None, stream=None):
     """Adjoint of :func:`fno_spectral_conv_fwd_cp`: dx and the factor gradients."""
-    ws, nb = _workspace(fno_workspace_size(desc, FNO_OP_SPECTRAL_BWD_CP), x.device, ws)
+    ws, nb = _workspace(fno_workspace_size(desc, FNO_OP_SPECTRAL_BWD_CP), x.device, ws, stream)
     _check(load().fno_spectral_conv_bwd_cp(ctypes.byref(desc), int(rank), _ptr(x), _ptr(lam),
                                            _ptr(A), _ptr(B), _ptr(C), _ptr(xhat_save), _ptr(dy),
                                            _ptr(dx), _ptr(dlam), _ptr(dA), _ptr(dB), _ptr(dC),
@@ -326,7 +335,7 @@ def fno_spectral_conv_bwd_cp(desc, rank, x, lam, A, B, C, xhat_save, dy, dx, dla
 def fno_block_bwd_cp(desc, rank, x, lam, A, B, C, W, pre_save, xhat_save, dy, dx, dlam, dA, dB,
                      dC, dW, db, ws=None, stream=None):
     """Adjoint of :func:`fno_block_fwd_cp`: dx, the factor gradients, dW and db."""
-    ws, nb = _workspace(fno_workspace_size(desc, FNO_OP_BLOCK_BWD_CP), x.device, ws)
+    ws, nb = _workspace(fno_workspace_size(desc, FNO_OP_BLOCK_BWD_CP), x.device, ws, stream)
     _check(load().fno_block_bwd_cp(ctypes.byref(desc), int(rank), _ptr(x), _ptr(lam), _ptr(A),
                                    _ptr(B), _ptr(C), _ptr(W), _ptr(pre_save), _ptr(xhat_save),
                                    _ptr(dy), _ptr(dx), _ptr(dlam), _ptr(dA), _ptr(dB), _ptr(dC),
@@ -335,7 +344,7 @@ def fno_block_bwd_cp(desc, rank, x, lam, A, B, C, W, pre_save, xhat_save, dy, dx
 
 
 def fno_block_bwd(desc, x, R, W, pre_save, xhat_save, dy, dx, dR, dW, db, ws=None, stream=None):
-    ws, nb = _workspace(fno_workspace_size(desc, FNO_OP_BLOCK_BWD), x.device, ws)
+    ws, nb = _workspace(fno_workspace_size(desc, FNO_OP_BLOCK_BWD), x.device, ws, stream)
     _check(load().fno_block_bwd(ctypes.byref(desc), _ptr(x), _ptr(R), _ptr(W), _ptr(pre_save),
                                 _ptr(xhat_save), _ptr(dy), _ptr(dx), _ptr(dR), _ptr(dW), _ptr(db),
                                 _ptr(ws), nb, _stream(stream)))
@@ -367,7 +376,7 @@ def make_grads(tensors: Dict[str, object]) -> Grads:
 
 
 def fno_forward(desc, a, params: Params, u, saves=None, ws=None, stream=None):
-    ws, nb = _workspace(fno_net_workspace_size(desc, FNO_OP_NET_FWD), a.device, ws)
+    ws, nb = _workspace(fno_net_workspace_size(desc, FNO_OP_NET_FWD), a.device, ws, stream)
     _check(load().fno_forward(ctypes.byref(desc), _ptr(a), ctypes.byref(params), _ptr(u),
                               _ptr(saves), _ptr(ws), nb, _stream(stream)))
     return u
@@ -378,7 +387,7 @@ def fno_backward(desc, a, params: Params, saves, du, grads: Grads, ws=None, stre
     """``ready``: optional list of n_layers + 2 ``torch.cuda.Event`` that the
     backward records as each gradient group becomes final (fno_backward_ready):
     the projection's, then the layers' from the last to the first, then the lift's."""
-    ws, nb = _workspace(fno_net_workspace_size(desc, FNO_OP_NET_BWD), a.device, ws)
+    ws, nb = _workspace(fno_net_workspace_size(desc, FNO_OP_NET_BWD), a.device, ws, stream)
     if ready is None:
         _check(load().fno_backward(ctypes.byref(desc), _ptr(a), ctypes.byref(params), _ptr(saves),
                                    _ptr(du), ctypes.byref(grads), _ptr(ws), nb, _stream(stream)))
@@ -552,18 +561,10 @@ def _check_tensor(t, name: str, dtype, numel: int, device: int) -> None:
 
 
 def _scratch(nbytes: int, like, ws, stream):
-    """The caller's workspace, or a fresh one on the device of `like` that is not
-    reused before the work of the given stream is done with it."""
-    import torch
-    if ws is not None:
-        if ws.get_device() != like.get_device():
-            raise ValueError(f"ws is on {ws.device}, expected {like.device}")
-        return ws, ws.numel() * ws.element_size()
-    ws, nb = _workspace(nbytes, like.device, None)
-    if stream is not None and ws.is_cuda:
-        ws.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                         else torch.cuda.ExternalStream(stream, device=like.device))
-    return ws, nb
+    """:func:`_workspace` on the device of `like`; one on another device is refused."""
+    if ws is not None and ws.get_device() != like.get_device():
+        raise ValueError(f"ws is on {ws.device}, expected {like.device}")
+    return _workspace(nbytes, like.device, ws, stream)
 
 
 def _run(fn, device: int, stream, *args) -> None:
