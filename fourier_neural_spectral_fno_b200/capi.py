@@ -701,7 +701,9 @@ class GradList:
 
 def grad_list(grads, out=None) -> GradList:
     """The list of gradients for :func:`fno_grad_norm` and :func:`fno_clip_grads`;
-    ``out``: tensors for the clipped gradients (default: in place)."""
+    ``out``: tensors for the clipped gradients (default: in place).  Tensors that share
+    memory with another one of the list are refused (a shared parameter's gradient
+    belongs into it once)."""
     return GradList(grads, out)
 
 

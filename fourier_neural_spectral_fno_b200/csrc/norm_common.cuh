@@ -175,6 +175,19 @@ __device__ __forceinline__ float ln_rstd(float q_mean, float e, float eps) {
   return 1.0f / sqrtf((var < 0.f ? 0.f : var) + eps);
 }
 
+// e = mean(x - m0) of a first mean m0 = sum / C of 16-bit values, from the residual of
+// that division in place of a sum over the deviations.  It leaves out what the sum itself
+// has lost.  That is nothing where it would show, for values within a factor of two: they
+// are whole multiples of one step, with 12 bits (float16) or 9 (bfloat16), and a sum of
+// ResidualChannels of them keeps within float32's 24.  Values farther apart have a
+// spread of at least |x| / (2 C^1/2), against which a sum's rounding is small.
+template <typename T> struct ResidualChannels { static constexpr int N = 0; };
+template <> struct ResidualChannels<__half> { static constexpr int N = 1 << 12; };
+template <> struct ResidualChannels<__nv_bfloat16> { static constexpr int N = 1 << 15; };
+__device__ __forceinline__ float ln_residual(float sum, float m0, int C, float inv_c) {
+  return fmaf(-(float)C, m0, sum) * inv_c;
+}
+
 #define FNO_DISPATCH_T(dtype, ...)                                \
   do {                                                            \
     if ((dtype) == DT_F32) {                                      \

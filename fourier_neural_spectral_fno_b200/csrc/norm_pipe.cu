@@ -288,6 +288,8 @@ __device__ __forceinline__ Walk<S> pipe_begin(unsigned char *smem, const PipeArg
 // The converted values stay in registers from the first sweep on (a word is read
 // and converted once).  The correction of the mean (norm.cu) serves the 16-bit types
 // as well: a point of equal values has no step of its own to outweigh the rounding.
+// (As a sum over the deviations in every type: from the residual, norm_common.cuh, 32 x 64
+// x 65536 bfloat16 took 101.9 us against 91.6, 8 x 100 x 65536 39.2 against 40.4.)
 template <typename S>
 __global__ void __launch_bounds__(S::threads, 1)
     k_ln_fwd_pipe(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my,
@@ -360,7 +362,7 @@ __global__ void __launch_bounds__(S::threads, 1)
       r[k] = ln_rstd(sum[k] * a.inv_c, ek, a.eps);
       m[k] = f2splat(r[k]);
       mean[k] += ek;
-      e[k] = f2splat(-ek);
+      e[k] = f2splat(-ek * r[k]);   // xh = (x - mean) r - e r
     }
     if (a.mean_out && w.part == 0) {
 #pragma unroll
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(S::threads, 1)
       const f32x2 ga = f2pack(gb.x, gb.y), be = f2pack(gb.z, gb.w);
 #pragma unroll
       for (int k = 0; k < N; ++k) {
-        v[i][k] = f2fma(f2mul(f2add(v[i][k], e[k]), m[k]), ga, be);
+        v[i][k] = f2fma(f2fma(v[i][k], m[k], e[k]), ga, be);
       }
       st_pairs<S>(st + 2 * S::KW * i * S::row, v[i]);
     }

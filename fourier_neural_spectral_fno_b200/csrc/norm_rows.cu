@@ -19,6 +19,7 @@ namespace fno {
 namespace {
 
 constexpr int kRowThreads = 256;
+constexpr int kPackedAbove = 32 * 24;   // 16-bit rows of whole pieces with more: packed
 
 // a group's place in its CTA and the sums over its threads
 struct Group {
@@ -118,13 +119,18 @@ __device__ __forceinline__ f32x2 masked(f32x2 v, int c, int C) {
 }
 
 // The converted values stay in registers (each is converted once); the next row's
-// pieces are on their way meanwhile.
+// pieces are on their way meanwhile.  The correction of the mean (norm.cu) comes from a
+// residual for 16-bit types where no row of the kernel has more channels than that is
+// exact for; as a sum over the deviations, as float32 needs it, it cost 2 to 5 % (20011
+// x 768 18.6 us against 18.0, 262144 x 64 20.2 against 19.5).
 template <typename T, int NV, bool SHIFT, int THREADS>
 __global__ void __launch_bounds__(THREADS)
     k_ln_fwd_rows(const T *x, const T *__restrict__ gamma, const T *__restrict__ beta, T *y,
                   float *__restrict__ mean, float *__restrict__ rstd, long long rows, int C,
                   int tpr, float inv_c, float eps) {
   constexpr int V = Rows<T>::V, H = V / 2;
+  constexpr int kMost = V == 8 && !SHIFT ? kPackedAbove : 24 * THREADS;   // channels
+  constexpr bool kResidual = kMost <= ResidualChannels<T>::N;
   __shared__ float red[512];
   Group gr{red, tpr, (int)(threadIdx.x & (tpr - 1)), (int)(threadIdx.x / tpr), 0};
   const int R = blockDim.x / tpr;
@@ -153,9 +159,9 @@ __global__ void __launch_bounds__(THREADS)
 #pragma unroll
     for (int j = 0; j < NV; ++j)
       load_piece<T, SHIFT>(nx[j], x + (row + G) * C, lo0 + j * hop, C, row + G < rows);
-    float m0 = pair_sum(f2add(s[0], s[1]));
-    gr.sum<1>(&m0);
-    m0 *= inv_c;
+    float sum = pair_sum(f2add(s[0], s[1]));
+    gr.sum<1>(&sum);
+    const float m0 = sum * inv_c;
     const f32x2 m = f2splat(-m0);
     s[0] = s[1] = f2splat(0.f);
 #pragma unroll
@@ -166,24 +172,25 @@ __global__ void __launch_bounds__(THREADS)
       for (int i = 0; i < H; ++i) {
         v[j][i] = f2add(v[j][i], m);
         if (!whole) v[j][i] = masked(v[j][i], lo + 2 * i, C);
-        e[i & 1] = f2add(e[i & 1], v[j][i]);
+        if (!kResidual) e[i & 1] = f2add(e[i & 1], v[j][i]);
         s[i & 1] = f2fma(v[j][i], v[j][i], s[i & 1]);
       }
     }
-    float q[2] = {pair_sum(f2add(s[0], s[1])), pair_sum(f2add(e[0], e[1]))};
-    gr.sum<2>(q);
-    const float ek = q[1] * inv_c, r = ln_rstd(q[0] * inv_c, ek, eps);
+    float q[2] = {pair_sum(f2add(s[0], s[1])), kResidual ? 0.f : pair_sum(f2add(e[0], e[1]))};
+    gr.sum<kResidual ? 1 : 2>(q);
+    const float ek = kResidual ? ln_residual(sum, m0, C, inv_c) : q[1] * inv_c;
+    const float r = ln_rstd(q[0] * inv_c, ek, eps);
     if (row < rows) {
       if (mean && gr.t == 0) {
         mean[row] = m0 + ek;
         rstd[row] = r;
       }
-      const f32x2 rr = f2splat(r), em = f2splat(-ek);
+      const f32x2 rr = f2splat(r), er = f2splat(-ek * r);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
 #pragma unroll
         for (int i = 0; i < H; ++i)
-          v[j][i] = f2fma(f2mul(f2add(v[j][i], em), rr), ga[j][i], be[j][i]);
+          v[j][i] = f2fma(f2fma(v[j][i], rr, er), ga[j][i], be[j][i]);
         store_piece<T, SHIFT>(v[j], y + row * C, lo0 + j * hop, C);
       }
     }
@@ -199,6 +206,7 @@ __global__ void __launch_bounds__(THREADS, (NV <= 4 ? 1280 : 1024) / THREADS)
                          T *y, float *__restrict__ mean, float *__restrict__ rstd, long long rows,
                          int C, int tpr, float inv_c, float eps) {
   constexpr int V = Rows<T>::V, H = V / 2;
+  constexpr bool kResidual = 4 * V * THREADS <= ResidualChannels<T>::N;
   __shared__ float red[512];
   Group gr{red, tpr, (int)(threadIdx.x & (tpr - 1)), (int)(threadIdx.x / tpr), 0};
   const long long row = (long long)blockIdx.x * (THREADS / tpr) + gr.r;
@@ -215,9 +223,9 @@ __global__ void __launch_bounds__(THREADS, (NV <= 4 ? 1280 : 1024) / THREADS)
     for (int i = 0; i < H; ++i) s[i & 1] = f2add(s[i & 1], v[i]);
     p[j].keep();
   }
-  float m0 = pair_sum(f2add(s[0], s[1]));
-  gr.sum<1>(&m0);
-  m0 *= inv_c;
+  float sum = pair_sum(f2add(s[0], s[1]));
+  gr.sum<1>(&sum);
+  const float m0 = sum * inv_c;
   const f32x2 m = f2splat(-m0);
   s[0] = s[1] = f2splat(0.f);
 #pragma unroll
@@ -227,21 +235,22 @@ __global__ void __launch_bounds__(THREADS, (NV <= 4 ? 1280 : 1024) / THREADS)
 #pragma unroll
       for (int i = 0; i < H; ++i) {
         v[i] = f2add(v[i], m);
-        e[i & 1] = f2add(e[i & 1], v[i]);
+        if (!kResidual) e[i & 1] = f2add(e[i & 1], v[i]);
         s[i & 1] = f2fma(v[i], v[i], s[i & 1]);
       }
       p[j].keep();
     }
   }
-  float q[2] = {pair_sum(f2add(s[0], s[1])), pair_sum(f2add(e[0], e[1]))};
-  gr.sum<2>(q);
-  const float ek = q[1] * inv_c, r = ln_rstd(q[0] * inv_c, ek, eps);
+  float q[2] = {pair_sum(f2add(s[0], s[1])), kResidual ? 0.f : pair_sum(f2add(e[0], e[1]))};
+  gr.sum<kResidual ? 1 : 2>(q);
+  const float ek = kResidual ? ln_residual(sum, m0, C, inv_c) : q[1] * inv_c;
+  const float r = ln_rstd(q[0] * inv_c, ek, eps);
   if (row >= rows) return;
   if (mean && gr.t == 0) {
     mean[row] = m0 + ek;
     rstd[row] = r;
   }
-  const f32x2 rr = f2splat(r), em = f2splat(-ek);
+  const f32x2 rr = f2splat(r), er = f2splat(-ek * r);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int lo = lo0 + j * hop;
@@ -252,8 +261,8 @@ __global__ void __launch_bounds__(THREADS, (NV <= 4 ? 1280 : 1024) / THREADS)
       p[j].get2(v);
 #pragma unroll
       for (int i = 0; i < H; ++i) {
-        v[i] = f2add(f2add(v[i], m), em);
-        v[i] = f2fma(f2mul(v[i], rr), ga[i], be[i]);
+        v[i] = f2fma(f2add(v[i], m), rr, er);
+        v[i] = f2fma(v[i], ga[i], be[i]);
       }
       store_piece<T, false>(v, y + row * C, lo, C);
     }
@@ -378,7 +387,7 @@ template <typename T> int row_pieces(const NormShape &s) {
 // 58.4 against 55.9).
 template <typename T> bool use_packed(const NormShape &s) {
   constexpr int V = Rows<T>::V;
-  return s.C % V == 0 && s.C > (V == 8 ? 32 : 256) * 24;
+  return s.C % V == 0 && s.C > (V == 8 ? kPackedAbove : 256 * 24);
 }
 
 // most pieces per thread: 24 values of a row forward (the packed form four 16-bit

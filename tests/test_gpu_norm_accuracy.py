@@ -25,7 +25,10 @@ CONSTANT = [(1, 41, 102400), (2, 61, 34400), (1, 63, 66600), (3, 7, 200008), (1,
             (2, 7, 257), (2, 41, 1023), (1, 63, 4099), (3, 97, 259), (1, 125, 777), (2, 30, 301),
             (2, 61, 64), (1, 125, 132), (3, 60, 35),
             (9, 56, 1), (5, 63, 1), (4, 448, 1), (3, 776, 1), (6, 1000, 1), (5, 1001, 1),
-            (2, 896, 1), (3, 3584, 1), (1, 1100, 5)]
+            (2, 896, 1), (3, 3584, 1), (1, 1100, 5), (2, 4096, 1), (3, 4095, 1), (2, 8191, 1),
+            (2, 8192, 1), (3, 6137, 1)]
+# more channels than the first sum of float16 values is exact for
+LONG = [(2, 8200, 1), (3, 12001, 1), (2, 16384, 1)]
 
 
 @pytest.mark.parametrize("shape", CONSTANT, ids=str)
@@ -33,7 +36,7 @@ CONSTANT = [(1, 41, 102400), (2, 61, 34400), (1, 63, 66600), (3, 7, 200008), (1,
 def test_layer_norm_constant_points_of_any_size(shape, dtype):
     """Points of C equal 16-bit values v give mean = v, y = beta and dgamma = 0.
 
-    Every partial sum k v has at most 11 + 12 significant bits: exact.  The first
+    Every partial sum k v has at most 11 + 13 significant bits: exact.  The first
     mean is off by the reciprocal's and the product's rounding, d = v - m0 with |d| <=
     2.1 u |v|, and is a few steps of v, so that its sums k d are exact; their mean e is
     off by 2.1 u |d|.  So mean = m0 + e lies within 5 u^2 |v| of v before its rounding,
@@ -72,15 +75,16 @@ def test_layer_norm_constant_points_of_any_size(shape, dtype):
     assert not bool(dg.any())
 
 
-@pytest.mark.parametrize("shape", CONSTANT, ids=str)
+@pytest.mark.parametrize("shape", CONSTANT + LONG, ids=str)
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 def test_layer_norm_points_of_one_step(shape, dtype):
     """C equal values but for one channel, which is a step of the type (in float32
     2^-10 of the value) away: y within (2 C + 16) u (1 + |xh|) |gamma| + 4 u |y|, as for
     any other point, since the deviations are corrected by their own mean.  (The first
-    mean is off by at most C u |v|, in float32, or 2.1 u |v|; the spread is at least
-    2^-10 |v| / C^1/2 or 2^-11 |v| / C^1/2: the square of their quotient, which enters
-    the variance with a relative error of C u, stays below one.)"""
+    mean is off by at most 2.1 u |v|, the sum of up to 2^13 values of 11 bits being exact,
+    or by the 20 additions that a value takes part in; the spread is at least 2^-11 |v| /
+    C^1/2: the square of their quotient, which enters the variance with a relative error
+    of C u, stays below one.)"""
     import torch
     outer, C, inner = shape
     g = torch.Generator(device="cuda").manual_seed(43)
@@ -181,3 +185,28 @@ def test_layer_norm_sums_over_many_channels(shape, dtype):
                               + xh.abs() * (gg * xh).abs().mean(1, keepdim=True))
     assert bool(((dx.double() - ref).abs()
                  <= tol + HALF[dtype] * (ref.abs() + tol) + TINY[dtype]).all())
+
+
+@pytest.mark.parametrize("channels", [63, 128, 768, 1000, 2047, 4095, 4096, 6137, 8184, 8192, 12001])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_layer_norm_rows_on_both_sides_of_a_power_of_two(channels, dtype):
+    """Rows of 1024 with one channel a step above and one a half step below, whose sum
+    needs the finest bits: y within the tolerance above."""
+    import torch
+    rows = 40
+    g = torch.Generator(device="cuda").manual_seed(67)
+    dt = torch_dtype(dtype)
+    eps = torch.finfo(dt).eps
+    x = torch.full((rows, channels), 1024.0, device="cuda", dtype=dt)
+    up = torch.randint(0, channels // 2, (rows, 1), generator=g, device="cuda")
+    down = torch.randint(channels // 2, channels, (rows, 1), generator=g, device="cuda")
+    x.scatter_(1, up, 1024 * (1 + eps)).scatter_(1, down, 1024 * (1 - eps / 2))
+    d = capi.layer_norm_desc(rows, channels, 1, dtype, EPS)
+    y = torch.empty_like(x)
+    capi.fno_layer_norm_fwd(d, x, None, None, y)
+    x6 = x.double()
+    rm = x6.mean(1, keepdim=True)
+    ry = (x6 - rm) / ((x6 - rm).square().mean(1, keepdim=True) + EPS).sqrt()
+    tol = (2 * channels + 16) * U * (1 + ry.abs()) + 4 * U * ry.abs()
+    tol = tol + HALF[dtype] * (ry.abs() + tol) + TINY[dtype]
+    assert bool(((y.double() - ry).abs() <= tol).all())
