@@ -287,15 +287,20 @@ __device__ __forceinline__ Walk<S> pipe_begin(unsigned char *smem, const PipeArg
 
 // The converted values stay in registers from the first sweep on (a word is read
 // and converted once).  The correction of the mean (norm.cu) serves the 16-bit types
-// as well: a point of equal values has no step of its own to outweigh the rounding.
-// (As a sum over the deviations in every type: from the residual, norm_common.cuh, 32 x 64
-// x 65536 bfloat16 took 101.9 us against 91.6, 8 x 100 x 65536 39.2 against 40.4.)
+// as well: a point of equal values has no step of its own to outweigh the rounding.  For
+// them it comes from the residual (norm_common.cuh): 19 x 99 x 2704 float16 7.6 us, as a
+// sum over the deviations 7.9; but for 33 to 64 channels, where many points are slower
+// with it (32 x 64 x 65536 bfloat16 101.5 against 92.1 us, 32 x 48 x 65536 76.7 against
+// 70.1; 40 x 41 x 20000 float16 29.1 against 30.2).
 template <typename S>
 __global__ void __launch_bounds__(S::threads, 1)
     k_ln_fwd_pipe(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my,
                   const __grid_constant__ PipeArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   constexpr int N = S::N;
+  constexpr bool kResidual =
+      S::CM <= ResidualChannels<typename S::T>::N && (S::CM < 48 || S::CM > 64);
+  constexpr int M = kResidual ? N : 2 * N;   // sums of the second sweep
   Cursor at;
   Walk<S> w = pipe_begin<S>(smem, a, &mx, nullptr, &my, at);
   const float4 *coef = reinterpret_cast<const float4 *>(smem + S::coef) + w.part;
@@ -310,7 +315,7 @@ __global__ void __launch_bounds__(S::threads, 1)
     unsigned char *tile = w.ring + (at.it % S::NS) * S::stage;
     unsigned char *st = tile + 2 * w.part * S::row + w.col * S::column + w.lane * 4;
     f32x2 v[S::pairs][N], s[N], e[N], m[N];
-    float sum[2 * N];
+    float sum[M];
 #pragma unroll
     for (int k = 0; k < N; ++k) s[k] = f2splat(0.f);
 #pragma unroll
@@ -326,10 +331,11 @@ __global__ void __launch_bounds__(S::threads, 1)
       w.drain(at.it);
       break;
     }
-    float mean[N];
+    float mean[N], res[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       mean[k] = sum[k] * a.inv_c;
+      if (kResidual) res[k] = ln_residual(sum[k], mean[k], C, a.inv_c);
       m[k] = f2splat(-mean[k]);
       s[k] = e[k] = f2splat(0.f);
     }
@@ -344,21 +350,21 @@ __global__ void __launch_bounds__(S::threads, 1)
           f2unpack(v[i][k], d0, d1);
           v[i][k] = f2pack(c < C ? d0 : 0.f, c + 1 < C ? d1 : 0.f);
         }
-        e[k] = f2add(e[k], v[i][k]);
+        if (!kResidual) e[k] = f2add(e[k], v[i][k]);
         s[k] = f2fma(v[i][k], v[i][k], s[k]);
       }
     }
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       sum[k] = pair_sum(s[k]);
-      sum[N + k] = pair_sum(e[k]);
+      if (!kResidual) sum[N + k] = pair_sum(e[k]);
     }
-    w.template exchange<2 * N>(sum, turn++, true);
+    w.template exchange<M>(sum, turn++, true);
     const long long n = (long long)at.seg * S::P + (w.col * 32 * S::W + w.lane) * S::E;
     float r[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      const float ek = sum[N + k] * a.inv_c;
+      const float ek = kResidual ? res[k] : sum[N + k] * a.inv_c;
       r[k] = ln_rstd(sum[k] * a.inv_c, ek, a.eps);
       m[k] = f2splat(r[k]);
       mean[k] += ek;
