@@ -562,9 +562,11 @@ def _check_tensor(t, name: str, dtype, numel: int, device: int) -> None:
 
 def _scratch(nbytes: int, like, ws, stream):
     """:func:`_workspace` on the device of `like`; one on another device is refused."""
-    if ws is not None and ws.get_device() != like.get_device():
+    if ws is None:
+        return _workspace(nbytes, like.device, None, stream)
+    if ws.get_device() != like.get_device():
         raise ValueError(f"ws is on {ws.device}, expected {like.device}")
-    return _workspace(nbytes, like.device, ws, stream)
+    return ws, ws.numel() * ws.element_size()
 
 
 def _run(fn, device: int, stream, *args) -> None:
