@@ -27,10 +27,12 @@ namespace {
 constexpr int OT = 128;   // threads per CTA where a warp holds all channels
 
 constexpr int odd_threads(int KW) { return KW > 1 ? 32 * KW : OT; }
-// Forward CTAs an SM that the compiler plans for.  For 20 channels seven: left alone it
-// fits 63 registers by loading in turns (12 x 20 x 48323 float16 16.4 us a pass on fresh
-// inputs against 15.1, float32 19.4 against 18.9).
-constexpr int odd_ctas(int CM, int KW) { return KW == 1 && CM == 20 ? 7 : 1; }
+// Forward CTAs an SM that the compiler plans for; 0: it chooses the registers by itself
+// (held to one CTA it takes up to 24 more: 4 x 128 x 44521 float32 41.1 us against 36.7).
+// With 20 channels seven, since by itself it then fits 63 registers by loading in turns
+// (12 x 20 x 48323 float16 16.4 us a pass on fresh inputs against 14.8, float32 19.4
+// against 18.9).
+constexpr int odd_ctas(int CM, int KW) { return KW == 1 && CM == 20 ? 7 : 0; }
 
 struct OddArgs {
   const void *x, *dy, *gamma, *beta;
