@@ -232,7 +232,7 @@ cudaError_t launch_ln_rows_fwd(const Launch &L, const NormShape &s, int dtype, c
 cudaError_t launch_ln_rows_bwd(const Launch &L, const NormShape &s, int dtype, const void *x,
                                const void *gamma, const float *mean, const float *rstd,
                                const void *dy, void *dx, float *partial, int *nparts);
-// the grid layout as a TMA pipeline, at most 64 channels (norm_pipe.cu)
+// the grid layout as a TMA pipeline, at most 128 channels (norm_pipe.cu)
 bool ln_pipe_supported(const NormShape &s, int dtype, bool bwd);
 cudaError_t launch_ln_pipe_fwd(const Launch &L, const NormShape &s, int dtype, const void *x,
                                const void *gamma, const void *beta, void *y, float *mean,

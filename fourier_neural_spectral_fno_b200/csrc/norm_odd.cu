@@ -13,11 +13,11 @@
 // kernels of norm_grid.cu, one point per lane with coefficients read from global
 // memory, took 48 instructions a value.  Copying a tile's whole 16-byte pieces
 // through shared memory, each row at its own offset, measured slower (29 us at 12 x
-// 20 x 48323 float16).  Measured there, against the element kernels: forward 14.2
-// and 19.6 us, backward 23.5 and 38; float32 forward 19.2 and 19.5, backward 28.4 and
-// 34.  4 x 64 x 44521: float16 forward 16.5 and 26.4, backward 29.2 and 43.5, float32
-// 18.7 and 24.9, 30.2 and 39.4; 4 x 128 x 44521: 37.4 and 50.2, 60.7 and 85.7, 38.6
-// and 47.9, 61.4 and 79.1.
+// 20 x 48323 float16).  Measured there, against the element kernels: forward 13.4
+// and 19.3 us, backward 23.7 and 37.9; float32 forward 18.9 and 19.4, backward 28.5 and
+// 34.1.  4 x 64 x 44521: float16 forward 16.2 and 26.4, backward 29.0 and 43.6, float32
+// 19.6 and 25.6, 30.3 and 39.5; 4 x 128 x 44521: 37.4 and 50.5, 63.0 and 86.1, 37.0
+// and 47.5, 62.9 and 79.2.
 #include "norm_common.cuh"
 
 namespace fno {
@@ -187,9 +187,9 @@ __global__ void __launch_bounds__(odd_threads(KW), odd_ctas(CM, KW)) k_ln_fwd_od
 }
 
 // Persistent: the channels' dgamma and dbeta sums stay in registers.  One point per
-// lane: with two the values of 20 channels cost half the warps (42 us against 28 at
-// 12 x 20 x 48323 float16).  EACH: CTAs an SM; where warps share the channels the
-// registers are held to what so many CTAs leave (4 x 64 x 44521 float32: 30.2 us,
+// lane: with two the values of 20 channels cost half the warps (and half again the time
+// at 12 x 20 x 48323 float16).  EACH: CTAs an SM; where warps share the channels the
+// registers are held to what so many CTAs leave (4 x 64 x 44521 float32: 30.3 us,
 // without that 40.4).
 template <typename T, int CM, int CLO, int KW, int EACH>
 __global__ void __launch_bounds__(odd_threads(KW), KW > 1 ? EACH : 1)
@@ -300,10 +300,11 @@ cudaError_t bwd_t(const Launch &L, const NormShape &s, OddArgs a, int *nparts) {
 
 }  // namespace
 
-// Rows that fill most of their tiles, tile numbers of 32 bits.  Backward float16 with
-// 8 channels, where a lane has few loads on their way, the element kernels are faster
-// (15 x 8 x 48323: 23.2 us against 27.9; float32 26.1 against 23.5; with 16 channels
-// 23.6 against 17.3).
+// Rows that fill most of their tiles, tile numbers of 32 bits.  Backward float16 with up
+// to 8 channels, where a lane has few loads on their way, goes to the element kernels
+// (15 x 8 x 48323: 20.4 us; 27.9 here, when that was tried; float32 23.1 there, 19.2
+// here).  With 16 channels float16 takes 33.4 us here and 39.1 there; float32, which
+// would gain a little there (32.9 against 37.4), follows the rule for 8 and for 20.
 bool ln_odd_supported(const NormShape &s, int dtype, bool bwd) {
   if (s.inner % (bwd && dtype != DT_F32 ? 8 : 4) == 0) return false;
   const long long segs = (s.inner + 31) / 32;
@@ -346,9 +347,11 @@ cudaError_t launch_ln_odd(const Launch &L, const NormShape &s, int dtype, const 
       else if (s.C <= 96) err = bwd_t<T, 12, 0, 8, 2>(L, s, a, nparts);
       else err = bwd_t<T, 8, 0, 16, 2>(L, s, a, nparts);
     } else {
-      // with shared channels one point a lane where the values are 4 bytes wide or a
-      // CTA has 16 of them (16 x 64 x 19881: float16 25.1 us with two, 28.3 with one;
-      // float32 32.2 and 29.7; 4 x 128 x 44521 float16 35.5 and 32.1)
+      // with shared channels one point a lane where the values are 4 bytes wide (16 x 64 x
+      // 19881: float16 26.0 us with two, 34.0 with one; float32 32.2 and 30.7; 4 x 90 x
+      // 44521: float16 24.9 and 28.9, float32 30.7 and 29.3), and in every type from 97
+      // channels on (4 x 128 x 44521 float32: 38.4 with two, 37.0 with one; float16,
+      // which two points would serve better, 29.9 and 37.4)
       if (s.C <= 8) err = fwd_t<T, 8, 1, 4>(L, s, a);
       else if (s.C <= 16) err = fwd_t<T, 16, 9, 4>(L, s, a);
       else if (s.C <= 20) err = fwd_t<T, 20, 17, 2>(L, s, a);

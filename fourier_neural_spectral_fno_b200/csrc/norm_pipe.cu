@@ -20,8 +20,8 @@
 // box is CM rows high.  Rows beyond C are filled with zeros, which add nothing to
 // the backward's sums (the forward's squares leave them out), and are not stored.
 //
-// Bound by HBM: 32 x 64 x 65536 bfloat16 backward 128.7 us with its parameters'
-// sums, 99 % of the copy rate; 2 x 20 x 128^3 float32 172.5 us, 93 %.
+// Bound by HBM: 32 x 64 x 65536 bfloat16 backward 128.2 us with its parameters'
+// sums, 99 % of the copy rate; 2 x 20 x 128^3 float32 169.3 us, 95 %.
 #include <cuda.h>
 
 #include "norm_common.cuh"
@@ -609,7 +609,7 @@ cudaError_t bwd_t(const Launch &L, const NormShape &s, const void *x, const void
 // were best nearly everywhere, the neighbours within 5 %; above 64 channels tiles
 // that leave room for two teams (8 x 100 x 65536 bfloat16: forward 39.1 us with two
 // teams of two columns, 42.7 with one of four; 16 warps a column 95 us backward,
-// four 63).
+// four 65).
 struct Cfg {
   int cm, w, kw, sg, mt;
 };
@@ -644,16 +644,17 @@ template <typename T, int I, int ARRAYS> struct ShapeOf {
 // numbers of 31 bits, strides the maps can hold; rows that fill most of their
 // tiles of up to 256 points; and enough work that the pipelines' start does not
 // show.  Against the register kernels (norm_grid.cu), us, with up to 64 channels:
-// backward float32 20 x 4096 at batch 8 / 16 / 32: 6.7 / 8.4 / 11.9 against
-// 5.9 / 8.5 / 12.1, 64 x 4096 at 2 / 4: 6.4 / 7.3 against 6.4 / 9.0; bfloat16
-// 20 x 4096 at 8 / 16: 7.4 / 7.2 against 7.8 / 10.2: from a million values on.
-// Forward bfloat16 20 x 4096 at 32 / 64: 5.2 / 7.1 against 4.5 / 7.7: from four
-// million; float32 never (16 x 32 x 65536: 51 against 44.8, 96 % of the copy rate).
+// backward float32 20 x 4096 at batch 8 / 16 / 32: 5.7 / 7.3 / 9.7 against
+// 5.0 / 6.2 / 9.1, 64 x 4096 at 2 / 4: 6.1 / 6.6 against 5.1 / 6.4; bfloat16
+// 20 x 4096 at 8 / 16: 6.1 / 6.3 against 5.5 / 7.5: from a million values on (20
+// channels of float32 gain later).
+// Forward bfloat16 20 x 4096 at 32 / 64: 5.4 / 7.4 against 4.5 / 7.5: from four
+// million; float32 never (16 x 32 x 65536: 51 against 44.5, 96 % of the copy rate).
 // With more channels, where the register kernels split a point's channels over a
 // CTA's warps, from a million values on in every direction and type: at 128 x 4096,
-// batch 4, and 128 x 65536, batch 8, forward bfloat16 5.4 and 49.9 against 7.2 and
-// 74.6, float32 5.1 and 97.5 against 8.6 and 112; backward bfloat16 7.4 and 70.3
-// against 7.9 and 139, float32 8.8 and 130 against 10.8 and 208.
+// batch 4, and 128 x 65536, batch 8, forward bfloat16 5.5 and 49.9 against 7.2 and
+// 74.7, float32 5.1 and 97.4 against 8.6 and 113; backward bfloat16 7.3 and 71.4
+// against 7.9 and 139, float32 8.5 and 130 against 10.1 and 208.
 bool ln_pipe_supported(const NormShape &s, int dtype, bool bwd) {
   if (!bwd && dtype == DT_F32 && s.C <= 64) return false;
   const long long es = dtype == DT_F32 ? 4 : 2, n = s.outer * s.C * s.inner;

@@ -9,9 +9,9 @@
 // over a row's ends are read and written value by value.  Sums go by shuffles
 // inside a warp and through shared memory between a row's warps (a named barrier
 // per group).  Groups walk over the rows: gamma and beta, and the backward's sums
-// of dgamma and dbeta, stay in registers.  20011 x 768 bfloat16 forward 17.8 us (53 %
+// of dgamma and dbeta, stay in registers.  20011 x 768 bfloat16 forward 18.1 us (53 %
 // of the copy rate), 262144 x 64 float32 24.7 (85 %); 4099 x 1001 float32 backward
-// 16.0: what is in flight, held by 16 warps an SM, bounds the rows, and HBM the rest.
+// 16.1: what is in flight, held by 16 warps an SM, bounds the rows, and HBM the rest.
 #include "norm_common.cuh"
 
 namespace fno {
@@ -297,9 +297,11 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS)
     nmu = in ? mean[row] : 0.f;
     nr = in ? rstd[row] : 0.f;
   };
-  // the next row on its way: with 16 values a thread the registers give more as
-  // a second CTA's (37.8 -> 33.6 us at 16384 x 1024 bfloat16; with fewer, one row
-  // ahead is 31.5 against 37.6 at 262144 x 64)
+  // The next row on its way where a thread has fewer than 16 values (262144 x 64:
+  // float32 37.8 us, without it 41.9; bfloat16 28.1 and 34.3).  With 16, float32's
+  // registers give more as a second CTA's (4099 x 1001: 16.1 us, with the next row
+  // 19.0); packed 16-bit rows could hold it (16384 x 1024 bfloat16 30.5 us, with the
+  // next row 25.9), which this rule leaves out.
   constexpr bool kAhead = NV * V < 16;
   if (kAhead) fetch(first);
 #pragma unroll
@@ -381,10 +383,10 @@ template <typename T> int row_pieces(const NormShape &s) {
 }
 
 // Rows for the packed forward: those that a warp does not hold, where it measured
-// faster than the one with converted values (bfloat16 16384 x 1024: 20.6 against
-// 24.0 us, 4096 x 8192: 36.8 against 53.5; 20011 x 768: 19.3 against 17.8), in
-// float32 only those of 512 threads (4096 x 8192: 67.4 against 76.0 us, 8192 x 4096:
-// 58.4 against 55.9).
+// faster than the one with converted values (bfloat16 16384 x 1024: 20.4 against
+// 24.0 us, 4096 x 8192: 37.0 against 53.5; 20011 x 768: 19.3 against 18.1), in
+// float32 only those of 512 threads (4096 x 8192: 66.7 against 76.0 us, 8192 x 4096:
+// 58.4 against 55.5).
 template <typename T> bool use_packed(const NormShape &s) {
   constexpr int V = Rows<T>::V;
   return s.C % V == 0 && s.C > (V == 8 ? kPackedAbove : 256 * 24);
