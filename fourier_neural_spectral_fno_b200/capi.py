@@ -484,7 +484,8 @@ def fno_adam_step(theta, m, v, grad, param_out, step: int, lr: float, beta1: flo
 
 class SkippedSteps:
     """The count of the steps that an optimiser skipped, on the device; handed to
-    :func:`fno_adam_step_clipped` in every step."""
+    :func:`fno_adam_step_clipped` once in every step (parameters that are updated by
+    several calls have a count each)."""
 
     def __init__(self, device):
         import torch

@@ -470,7 +470,8 @@ int fno_adam_step_clipped(int64_t n, float *theta, float *m, float *v, const flo
  * and t = step - (steps skipped before), so that a skipped step leaves no trace
  * in the next one's bias correction.  skipped: device, four int32, zeroed before
  * the first call; [0] is the number of steps skipped so far, [1..3] are the
- * library's.  One step's calls and the next's follow one another on a stream. */
+ * library's.  One call a step: parameters updated by several calls have a count
+ * each.  The calls of one count follow one another (one stream, or ordered). */
 int fno_adam_step_skipping(int64_t n, float *theta, float *m, float *v, const float *grad,
                            void *param_out, int out_dtype, int step, float lr, float beta1,
                            float beta2, float eps, float weight_decay, float grad_scale,
