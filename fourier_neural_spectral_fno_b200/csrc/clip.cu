@@ -282,20 +282,6 @@ int fill(TensorTable<N> &tab, int at, int n, const void *const *in, void *const 
   return i;
 }
 
-#define FNO_DISPATCH_T(dtype, ...)                                \
-  do {                                                            \
-    if ((dtype) == DT_F32) {                                      \
-      using T = float;                                            \
-      __VA_ARGS__;                                                \
-    } else if ((dtype) == DT_F16) {                               \
-      using T = __half;                                           \
-      __VA_ARGS__;                                                \
-    } else {                                                      \
-      using T = __nv_bfloat16;                                    \
-      __VA_ARGS__;                                                \
-    }                                                             \
-  } while (0)
-
 int clip_grid(const Launch &L, int chunks) {
   const int ctas = (chunks + CT / 32 - 1) / (CT / 32);
   int cap = 4 * L.num_sms;

@@ -54,6 +54,21 @@ void set_last_error(const char *fmt, ...);
 void launch_begin(const Launch &L);
 void launch_end(const Launch &L, const char *tag);
 
+// the statement with T as the storage dtype's type
+#define FNO_DISPATCH_T(dtype, ...)                                \
+  do {                                                            \
+    if ((dtype) == DT_F32) {                                      \
+      using T = float;                                            \
+      __VA_ARGS__;                                                \
+    } else if ((dtype) == DT_F16) {                               \
+      using T = __half;                                           \
+      __VA_ARGS__;                                                \
+    } else {                                                      \
+      using T = __nv_bfloat16;                                    \
+      __VA_ARGS__;                                                \
+    }                                                             \
+  } while (0)
+
 // A launch that may begin while the one before it still runs: the kernel waits for
 // that one's results with cudaGridDependencySynchronize.
 template <typename... P, typename... A>

@@ -540,20 +540,6 @@ int pointwise_grid(long long total, int num_sms) {
 
 }  // namespace
 
-#define FNO_DISPATCH_T(dtype, ...)                                \
-  do {                                                            \
-    if ((dtype) == DT_F32) {                                      \
-      using T = float;                                            \
-      __VA_ARGS__;                                                \
-    } else if ((dtype) == DT_F16) {                               \
-      using T = __half;                                           \
-      __VA_ARGS__;                                                \
-    } else {                                                      \
-      using T = __nv_bfloat16;                                    \
-      __VA_ARGS__;                                                \
-    }                                                             \
-  } while (0)
-
 cudaError_t launch_lift(const Launch &L, const Geom &g, int dtype, int in_ch, int width,
                         const void *a, const void *P, const void *p, void *v) {
   const size_t vb = dtype == DT_F32 ? 16 : 8;   // vector bytes of 4 elements

@@ -166,6 +166,13 @@ __device__ __forceinline__ long long again(long long v) {
   return v;
 }
 
+// the sum of a pair's halves
+__device__ __forceinline__ float pair_sum(f32x2 v) {
+  float a, b;
+  f2unpack(v, a, b);
+  return a + b;
+}
+
 template <typename T> struct VecOf { static constexpr int N = 16 / sizeof(T); };
 
 // 1 / sqrt(var + eps) with var = q / C - e^2 from the deviations about a first
@@ -187,20 +194,6 @@ template <> struct ResidualChannels<__nv_bfloat16> { static constexpr int N = 1 
 __device__ __forceinline__ float ln_residual(float sum, float m0, int C, float inv_c) {
   return fmaf(-(float)C, m0, sum) * inv_c;
 }
-
-#define FNO_DISPATCH_T(dtype, ...)                                \
-  do {                                                            \
-    if ((dtype) == DT_F32) {                                      \
-      using T = float;                                            \
-      __VA_ARGS__;                                                \
-    } else if ((dtype) == DT_F16) {                               \
-      using T = __half;                                           \
-      __VA_ARGS__;                                                \
-    } else {                                                      \
-      using T = __nv_bfloat16;                                    \
-      __VA_ARGS__;                                                \
-    }                                                             \
-  } while (0)
 
 // ---- per-layout kernels -----------------------------------------------------
 // grid layout (inner > 1), values held in registers (norm_grid.cu)

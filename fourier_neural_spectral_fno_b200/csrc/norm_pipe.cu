@@ -124,12 +124,6 @@ template <typename S> __device__ __forceinline__ void st_pairs(unsigned char *at
 // keeps the values of the sweep before in registers (and spills them).
 __device__ __forceinline__ void sweep() { __syncwarp(); }
 
-__device__ __forceinline__ float pair_sum(f32x2 v) {
-  float a, b;
-  f2unpack(v, a, b);
-  return a + b;
-}
-
 // A place in a team's walk over its tiles: the walk's tile `it` is
 // first + it stride, sample b, tile `seg` of its row of segs.
 struct Cursor {

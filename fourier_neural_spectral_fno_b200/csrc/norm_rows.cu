@@ -105,12 +105,6 @@ __device__ __forceinline__ void load_coef(f32x2 *p, const T *w, int lo, int C, f
   }
 }
 
-__device__ __forceinline__ float pair_sum(f32x2 v) {
-  float a, b;
-  f2unpack(v, a, b);
-  return a + b;
-}
-
 // a pair's halves where their columns lie in the row, else 0
 __device__ __forceinline__ f32x2 masked(f32x2 v, int c, int C) {
   float a, b;
